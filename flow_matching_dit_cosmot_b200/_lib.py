@@ -34,6 +34,8 @@ COSMOT_EPI_RES_F32 = 2
 COSMOT_MASK_FULL = 0
 COSMOT_MASK_BLOCK_CAUSAL = 1
 COSMOT_ATTN_NO_TILE_SKIP = 1
+COSMOT_KV8_FULL = 0
+COSMOT_KV8_CAUSAL = 1
 COSMOT_SITE_SELFTEST = 900
 COSMOT_SITE_SELFTEST_BOUNDS = 901
 
@@ -67,6 +69,18 @@ class AttnDesc(ctypes.Structure):
                 ("chunk", c_vp), ("batch", c_i32), ("flags", c_i32),
                 ("q_batch_stride", c_i64), ("kv_batch_stride", c_i64), ("o_batch_stride", c_i64),
                 ("softmax_scale", c_f32), ("reserved2", c_f32)]
+
+
+class Kv8Cache(ctypes.Structure):
+    _fields_ = [("k", c_vp), ("v", c_vp), ("k_scale", c_vp), ("v_scale", c_vp), ("lens", c_vp), ("ld", c_i64),
+                ("batch_stride", c_i64), ("batch", c_i32), ("capacity", c_i32), ("n_kv_heads", c_i32),
+                ("head_dim", c_i32), ("block", c_i32), ("reserved", c_i32)]
+
+
+class Kv8Query(ctypes.Structure):
+    _fields_ = [("n_q", c_i64), ("q_batch_stride", c_i64), ("o_batch_stride", c_i64), ("n_heads", c_i32),
+                ("n_new", c_i32), ("mask_mode", c_i32), ("max_len", c_i32), ("softmax_scale", c_f32),
+                ("reserved", c_i32)]
 
 
 class Dims(ctypes.Structure):
@@ -122,6 +136,13 @@ SIGNATURES = {
                                            ctypes.c_size_t, c_vp]),
     "cosmot_attention_split_workspace": (c_i32, [_P(AttnDesc), c_i32, _P(ctypes.c_size_t)]),
     "cosmot_attention_kv_split": (c_i32, [_P(AttnDesc)]),
+    "cosmot_kv8_store": (c_i32, [_P(Kv8Cache), c_vp, c_vp, c_i64, c_i64, c_i32, c_vp]),
+    "cosmot_kv8_attention_workspace": (c_i32, [_P(Kv8Cache), _P(Kv8Query), _P(ctypes.c_size_t)]),
+    "cosmot_kv8_attention": (c_i32, [_P(Kv8Cache), _P(Kv8Query), c_vp, c_i64, c_vp, c_i64, c_vp, c_vp,
+                                     ctypes.c_size_t, c_vp]),
+    "cosmot_kv8_weigh": (c_i32, [_P(Kv8Cache), _P(Kv8Query), c_vp, c_i64, c_vp, c_f32, c_vp, c_vp]),
+    "cosmot_kv8_evict_workspace": (c_i32, [_P(Kv8Cache), _P(ctypes.c_size_t)]),
+    "cosmot_kv8_evict": (c_i32, [_P(Kv8Cache), c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, ctypes.c_size_t, c_vp]),
     "cosmot_flow_euler_step": (c_i32, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_i64, c_f64, c_f64, c_vp]),
     "cosmot_flow_cfg_euler_step": (c_i32, [c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_i64, c_f64, c_f64, c_f64,
                                            c_vp]),
@@ -310,6 +331,43 @@ def cosmot_mot_mask_export(desc: AttnDesc, tile_codes: int, visible: int = 0, st
     (uint8 device buffers) of the attention kernel's masking."""
     return _call("cosmot_mot_mask_export", ctypes.byref(desc), c_vp(tile_codes), c_vp(visible or None),
                  c_vp(stream), check=check)
+
+
+def cosmot_kv8_store(cache: Kv8Cache, k: int, v: int, ld_src: int, src_batch_stride: int, n_rows: int,
+                     stream: int = 0, check=True):
+    return _call("cosmot_kv8_store", ctypes.byref(cache), c_vp(k), c_vp(v), ld_src, src_batch_stride, n_rows,
+                 c_vp(stream), check=check)
+
+
+def cosmot_kv8_attention_workspace(cache: Kv8Cache, query: Kv8Query) -> int:
+    n = ctypes.c_size_t(0)
+    _call("cosmot_kv8_attention_workspace", ctypes.byref(cache), ctypes.byref(query), ctypes.byref(n))
+    return n.value
+
+
+def cosmot_kv8_attention(cache: Kv8Cache, query: Kv8Query, q: int, ld_q: int, o: int, ld_o: int, lse: int = 0,
+                         workspace: int = 0, workspace_bytes: int = 0, stream: int = 0, check=True):
+    return _call("cosmot_kv8_attention", ctypes.byref(cache), ctypes.byref(query), c_vp(q), ld_q, c_vp(o), ld_o,
+                 c_vp(lse or None), c_vp(workspace or None), workspace_bytes, c_vp(stream), check=check)
+
+
+def cosmot_kv8_weigh(cache: Kv8Cache, query: Kv8Query, q: int, ld_q: int, lse: int, decay: float, weight: int,
+                     stream: int = 0, check=True):
+    return _call("cosmot_kv8_weigh", ctypes.byref(cache), ctypes.byref(query), c_vp(q), ld_q, c_vp(lse), decay,
+                 c_vp(weight), c_vp(stream), check=check)
+
+
+def cosmot_kv8_evict_workspace(cache: Kv8Cache) -> int:
+    n = ctypes.c_size_t(0)
+    _call("cosmot_kv8_evict_workspace", ctypes.byref(cache), ctypes.byref(n))
+    return n.value
+
+
+def cosmot_kv8_evict(cache: Kv8Cache, weight: int, keep_blocks: int, first_rows: int, last_rows: int,
+                     weight_out: int, lens_out: int, workspace: int, workspace_bytes: int, stream: int = 0,
+                     check=True):
+    return _call("cosmot_kv8_evict", ctypes.byref(cache), c_vp(weight), keep_blocks, first_rows, last_rows,
+                 c_vp(weight_out), c_vp(lens_out), c_vp(workspace or None), workspace_bytes, c_vp(stream), check=check)
 
 
 def cosmot_flow_euler_step(x: int, ld_x: int, v: int, ld_v: int, row_begin: int, row_end: int, n_cols: int,

@@ -238,3 +238,205 @@ class MoTStack:
         else:
             L.cosmot_stack_forward_io(self.dims, self.cw, seq, ptr(h), ptr(h_out), sigma, sigma_next, io, ptr(ws),
                                       ws.numel(), stream_handle(stream))
+
+
+def _rows_layout(t: torch.Tensor, name: str, batch: int, heads: Optional[int], head_dim: int, dtype, n: Optional[int] = None):
+    """(ld, rows between sequences) of a [batch, n, heads, head_dim] tensor whose
+    rows hold their heads side by side; a view of a wider row (the columns of a
+    QKV projection) fits."""
+    if t.dim() != 4 or t.shape[0] != batch or t.shape[3] != head_dim or (heads is not None and t.shape[2] != heads) or \
+            (n is not None and t.shape[1] != n):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{batch}, {'n' if n is None else n}, "
+                         f"{'heads' if heads is None else heads}, {head_dim}]")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    h, rows = t.shape[2], t.shape[1]
+    s0, s1, s2, s3 = t.stride()
+    width = h * head_dim
+    if t.numel() == 0:
+        return width, rows
+    if s3 != 1 or (h > 1 and s2 != head_dim):
+        raise ValueError(f"{name}: a row's heads must lie side by side (strides {t.stride()})")
+    if rows == 1:  # the stride of a dimension of one says nothing
+        ld, between = (s0, 1) if batch > 1 else (width, 1)
+    else:
+        ld, between = s1, rows
+        if batch > 1:
+            if ld <= 0 or s0 % ld:
+                raise ValueError(f"{name}: the batch stride must be a whole number of rows (strides {t.stride()})")
+            between = s0 // ld
+    if ld < width or between < rows:
+        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+    return ld, between
+
+
+class KVCache8:
+    """A key/value cache in 8 bits: e4m3 rows with one float32 scale for each
+    block of rows and key head (see cosmot_kv8_cache).
+
+    Wraps the caller's tensors: k, v float8_e4m3fn [batch, capacity, n_kv_heads,
+    head_dim]; k_scale, v_scale float32 [batch, n_kv_heads, blocks], blocks =
+    ceil(capacity / block); lens int32 [batch], the rows each sequence holds.
+    `KVCache8.empty` makes them.  A streaming step:
+
+        cache.store(k, v)                              # behind the rows held
+        o, lse = cache.attend(q, n_new=n)              # over them and the new ones
+        cache.weigh(q, lse, weight, n_new=n)           # optional: what got attention
+        cache.advance(n)                               # after the last denoising step
+        cache.evict(weight, keep_blocks, first_rows=n_ar, last_rows=n)
+
+    Every call runs on `stream` (default: the current one of the cache's device)
+    and follows `lens` on the device, so it may be captured into a CUDA graph.
+    The library reports lengths outside the cache through the device status.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                 lens: torch.Tensor, block: int):
+        _need_cuda(k, v, k_scale, v_scale, lens)
+        if k.dim() != 4:
+            raise ValueError(f"k has shape {tuple(k.shape)}, expected [batch, capacity, n_kv_heads, head_dim]")
+        batch, capacity, n_kv, hd = k.shape
+        if block not in (16, 32, 64, 128):
+            raise ValueError(f"block {block}: 16, 32, 64 or 128")
+        layout = _rows_layout(k, "k", batch, n_kv, hd, torch.float8_e4m3fn)
+        if _rows_layout(v, "v", batch, n_kv, hd, torch.float8_e4m3fn, capacity) != layout:
+            raise ValueError("k and v must have the same strides")
+        self.n_blocks = -(-capacity // block)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            self._check(name, t, torch.float32, (batch, n_kv, self.n_blocks))
+        self._check("lens", lens, torch.int32, (batch,))
+        if len({t.device for t in (k, v, k_scale, v_scale, lens)}) != 1:
+            raise ValueError("the cache's tensors must be on one device")
+        self.k, self.v, self.k_scale, self.v_scale, self.lens, self.block = k, v, k_scale, v_scale, lens, block
+        self.batch, self.capacity, self.n_kv_heads, self.head_dim = batch, capacity, n_kv, hd
+        self.device = k.device
+        self.desc = L.Kv8Cache(ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), ptr(lens), layout[0], layout[1], batch,
+                               capacity, n_kv, hd, block, 0)
+
+    @classmethod
+    def empty(cls, batch: int, capacity: int, n_kv_heads: int, head_dim: int, block: int = 64, device="cuda"):
+        rows = lambda: torch.zeros((batch, capacity, n_kv_heads, head_dim), dtype=torch.uint8,  # noqa: E731
+                                   device=device).view(torch.float8_e4m3fn)
+        scales = lambda: torch.ones((batch, n_kv_heads, -(-capacity // block)), device=device)  # noqa: E731
+        return cls(rows(), rows(), scales(), scales(), torch.zeros((batch,), dtype=torch.int32, device=device), block)
+
+    def empty_weight(self) -> torch.Tensor:
+        """Accumulated weights for weigh / evict, all zero."""
+        return torch.zeros((self.batch, self.n_kv_heads, self.n_blocks), device=self.device)
+
+    @staticmethod
+    def _check(name, t, dtype, shape):
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} (got {t.dtype}, "
+                             f"{tuple(t.shape)}, {'contiguous' if t.is_contiguous() else 'strided'})")
+
+    def _here(self, *named):
+        for name, t in named:
+            if t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
+
+    def _stream(self, stream, *made):
+        """The stream's handle; tensors made here are kept until it is done with them."""
+        if stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        if stream.device != self.device:
+            raise ValueError(f"the stream is on {stream.device}, the cache on {self.device}")
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+        return stream.cuda_stream
+
+    def _workspace(self, need: int, workspace: Optional[torch.Tensor]):
+        """(tensor, made here): the caller's workspace, or one for this call."""
+        if workspace is not None:
+            self._here(("workspace", workspace))
+            if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
+                raise ValueError(f"workspace: expected at least {need} contiguous uint8 elements")
+            return workspace, None
+        made = torch.empty((need,), dtype=torch.uint8, device=self.device) if need else None
+        return made, made
+
+    def _query(self, q: torch.Tensor, n_new: int, causal: bool, max_len: int, softmax_scale: float):
+        ld, between = _rows_layout(q, "q", self.batch, None, self.head_dim, torch.bfloat16)
+        self._here(("q", q))
+        desc = L.Kv8Query(q.shape[1], between, q.shape[1], q.shape[2], n_new,
+                          L.COSMOT_KV8_CAUSAL if causal else L.COSMOT_KV8_FULL, max_len, softmax_scale, 0)
+        return desc, ld
+
+    def advance(self, n: int):
+        """The last n stored rows become rows held (on the current stream)."""
+        self.lens.add_(n)
+
+    def store(self, k: torch.Tensor, v: torch.Tensor, stream=None):
+        """Rows [batch, n, n_kv_heads, head_dim] (bf16, views of a QKV projection
+        fit) behind the ones held; `advance` makes them held."""
+        layout = _rows_layout(k, "k", self.batch, self.n_kv_heads, self.head_dim, torch.bfloat16)
+        if _rows_layout(v, "v", self.batch, self.n_kv_heads, self.head_dim, torch.bfloat16, k.shape[1]) != layout:
+            raise ValueError("k and v must have the same strides")
+        self._here(("k", k), ("v", v))
+        if k.shape[1] == 0:
+            return
+        with torch.cuda.device(self.device):
+            L.cosmot_kv8_store(self.desc, ptr(k), ptr(v), layout[0], layout[1], k.shape[1], self._stream(stream))
+
+    def attend(self, q: torch.Tensor, n_new: int = 0, causal: bool = False, out: Optional[torch.Tensor] = None,
+               lse: Optional[torch.Tensor] = None, max_len: int = 0, softmax_scale: float = 0.0,
+               workspace: Optional[torch.Tensor] = None, stream=None):
+        """(o, lse) of q [batch, n, n_heads, head_dim] bf16 over the rows held and
+        n_new more: o as q, lse float32 [batch, n_heads, n] (natural log).  causal:
+        query i is row len - n + i and sees the rows up to itself; otherwise every
+        row.  max_len: the most rows any sequence shows, if known (it sizes the
+        split of the work only)."""
+        desc, ld = self._query(q, n_new, causal, max_len, softmax_scale)
+        made = []
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
+            made.append(out)
+        if lse is None:
+            lse = torch.empty((self.batch, q.shape[2], q.shape[1]), device=self.device)
+            made.append(lse)
+        ld_o, desc.o_batch_stride = _rows_layout(out, "out", self.batch, q.shape[2], self.head_dim, torch.bfloat16,
+                                                 q.shape[1])
+        self._check("lse", lse, torch.float32, (self.batch, q.shape[2], q.shape[1]))
+        self._here(("out", out), ("lse", lse))
+        if q.shape[1] == 0:
+            return out, lse
+        with torch.cuda.device(self.device):
+            need = L.cosmot_kv8_attention_workspace(self.desc, desc)
+            ws, fresh = self._workspace(need, workspace)
+            L.cosmot_kv8_attention(self.desc, desc, ptr(q), ld, ptr(out), ld_o, ptr(lse), ptr(ws),
+                                   0 if ws is None else ws.numel(), self._stream(stream, *made, fresh))
+        return out, lse
+
+    def weigh(self, q: torch.Tensor, lse: torch.Tensor, weight: torch.Tensor, decay: float = 1.0, n_new: int = 0,
+              causal: bool = False, max_len: int = 0, softmax_scale: float = 0.0, stream=None) -> torch.Tensor:
+        """weight [batch, n_kv_heads, blocks] = decay * weight + the attention
+        weight of q's rows for each block; lse as `attend` gave it for the same
+        query.  Returns weight."""
+        desc, ld = self._query(q, n_new, causal, max_len, softmax_scale)
+        desc.o_batch_stride = desc.n_q
+        self._check("lse", lse, torch.float32, (self.batch, q.shape[2], q.shape[1]))
+        self._check("weight", weight, torch.float32, (self.batch, self.n_kv_heads, self.n_blocks))
+        self._here(("lse", lse), ("weight", weight))
+        if q.shape[1] == 0:
+            raise ValueError("weigh needs at least one query")
+        with torch.cuda.device(self.device):
+            L.cosmot_kv8_weigh(self.desc, desc, ptr(q), ld, ptr(lse), decay, ptr(weight), self._stream(stream))
+        return weight
+
+    def evict(self, weight: torch.Tensor, keep_blocks: int, first_rows: int = 0, last_rows: int = 0,
+              in_place: bool = True, workspace: Optional[torch.Tensor] = None, stream=None):
+        """Brings every sequence and key head down to keep_blocks blocks of rows:
+        the ones that hold the first first_rows or the last last_rows rows, or a
+        part of a block, then those of the most weight.  The cache's rows and
+        scales move up in place; (weight, lens) follow in place too, or, with
+        in_place=False, are returned as new tensors."""
+        self._check("weight", weight, torch.float32, (self.batch, self.n_kv_heads, self.n_blocks))
+        self._here(("weight", weight))
+        w_out, lens = (weight, self.lens) if in_place else (torch.empty_like(weight), torch.empty_like(self.lens))
+        with torch.cuda.device(self.device):
+            ws, fresh = self._workspace(L.cosmot_kv8_evict_workspace(self.desc), workspace)
+            made = (fresh,) if in_place else (fresh, w_out, lens)
+            L.cosmot_kv8_evict(self.desc, ptr(weight), keep_blocks, first_rows, last_rows, ptr(w_out), ptr(lens),
+                               ptr(ws), ws.numel(), self._stream(stream, *made))
+        return w_out, lens

@@ -25,6 +25,9 @@ enum Where : int {
   kWhereAttnStore = 204,
   kWhereNormStore = 300,
   kWhereEulerStore = 301,
+  // 8-bit cache: a length outside its capacity, and the debug build's store checks
+  kWhereKv8Lens = 400,
+  kWhereKv8Store = 401,
   kWhereSelftest = COSMOT_SITE_SELFTEST,
   kWhereSelftestBounds = COSMOT_SITE_SELFTEST_BOUNDS,
 };

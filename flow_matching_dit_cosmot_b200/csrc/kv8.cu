@@ -1,0 +1,501 @@
+// The 8-bit key/value cache: storing rows, evicting blocks, and the argument
+// checks and dispatch of its attention and weighing.
+#include "kv8.cuh"
+
+namespace cosmot {
+namespace kv8 {
+
+// ------------------------------------------------------------------ store
+// One CTA per (block of rows, sequence x head, K or V).  Each thread owns
+// kUnits units of 16 elements: 32 bytes read, 16 written.  The block's largest
+// magnitude is reduced over the CTA, then the elements, still in registers,
+// are rounded against the scale, so every input byte is read once.  Rows of
+// the block that were there before are read only if the scale grows.
+// bound: HBM (4 bytes read and 2 written for each K and V element).
+template <int kUnits>
+__global__ void __launch_bounds__(256) store_kernel(const Cache c, const __nv_bfloat16* __restrict__ ksrc,
+                                                    const __nv_bfloat16* __restrict__ vsrc, int64_t ld_src,
+                                                    int64_t src_bstride, int32_t n, int* status) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ float part[8];
+  const int32_t b = blockIdx.y / c.n_kv, g = blockIdx.y % c.n_kv;
+  const int32_t held = c.lens[b];
+  if (held < 0 || held > c.capacity - n) {
+    if (threadIdx.x == 0) latch_status(status, COSMOT_ERR_BOUNDS, kWhereKv8Lens);
+    return;
+  }
+  const int32_t blk = held / c.block + (int32_t)blockIdx.x;
+  const int32_t row0 = blk * c.block, end = held + n;
+  if (row0 >= end) return;
+  const bool is_v = blockIdx.z != 0;
+  const __nv_bfloat16* src = (is_v ? vsrc : ksrc) + (int64_t)b * src_bstride * ld_src + (int64_t)g * c.hd;
+  uint8_t* dst = (is_v ? c.v : c.k) + (int64_t)b * c.bstride * c.ld + (int64_t)g * c.hd;
+  float* scale = (is_v ? c.v_scale : c.k_scale) + (int64_t)blockIdx.y * c.n_blocks + blk;
+  const int per_row = c.hd >> 4;  // units a row
+
+  uint4 x[kUnits][2];
+  float amax = 0.f;
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const int unit = (int)threadIdx.x + u * (int)blockDim.x;
+    const int32_t row = row0 + unit / per_row;
+    x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+    if (row >= held && row < end) {
+      const uint4* p = reinterpret_cast<const uint4*>(src + (int64_t)(row - held) * ld_src + (unit % per_row) * 16);
+      x[u][0] = __ldg(p);
+      x[u][1] = __ldg(p + 1);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(x[u]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = unpack_bf16x2(w[i]);
+      // infinities saturate like any other large value and NaN stays NaN: neither sets the scale
+      const float a = fabsf(f.x), d = fabsf(f.y);
+      if (a < INFINITY) amax = fmaxf(amax, a);
+      if (d < INFINITY) amax = fmaxf(amax, d);
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+  const float old = row0 < held ? *scale : 0.f;  // read by every thread before thread 0 writes it
+  __syncthreads();
+  for (int i = 0; i < (int)blockDim.x >> 5; ++i) amax = fmaxf(amax, part[i]);
+  const float fresh = exp2_int(scale_exponent(amax));
+  const bool have_old = old > 0.f && old < INFINITY;
+  const float now = have_old && old > fresh ? old : fresh;
+  const bool again = have_old && now > old;  // the rows that were there are rounded again
+  const float inv = 1.f / now;
+  if (threadIdx.x == 0 && dcheck(blk < c.n_blocks, status, kWhereKv8Store)) *scale = now;
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const int unit = (int)threadIdx.x + u * (int)blockDim.x;
+    const int32_t row = row0 + unit / per_row;
+    if (row >= end || (row < held && !again)) continue;
+    uint4* out = reinterpret_cast<uint4*>(dst + (int64_t)row * c.ld + (unit % per_row) * 16);
+    uint32_t y[4];
+    if (row >= held) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(x[u]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f0 = unpack_bf16x2(w[2 * i]), f1 = unpack_bf16x2(w[2 * i + 1]);
+        y[i] = (uint32_t)f32x2_to_e4m3x2(f0.x * inv, f0.y * inv) |
+               ((uint32_t)f32x2_to_e4m3x2(f1.x * inv, f1.y * inv) << 16);
+      }
+    } else {
+      const uint4 o4 = *out;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&o4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a = cvt_lo(w[i]), d = cvt_hi(w[i]);
+        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&a));
+        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&d));
+        y[i] = (uint32_t)f32x2_to_e4m3x2(f0.x * old * inv, f0.y * old * inv) |
+               ((uint32_t)f32x2_to_e4m3x2(f1.x * old * inv, f1.y * old * inv) << 16);
+      }
+    }
+    if (dcheck(row < c.capacity, status, kWhereKv8Store)) *out = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+}
+
+// ------------------------------------------------------------------ evict
+// Two kernels.  The first, one CTA per (sequence, head), finds which blocks
+// stay: a radix select over the ordered bits of the weights (four passes of 8
+// bits), then one pass in index order that keeps what is above the threshold,
+// the first ones equal to it, and the fixed blocks.  The second moves them.
+constexpr int kSelectThreads = 512;
+
+struct EvictPlan {  // per sequence, in the workspace
+  int32_t len, nb, count, reserved;
+};
+
+// Orders like torch's descending sort: NaN above infinity, both zeros equal.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cache c, const float* __restrict__ weight,
+                                                                     int32_t keep, int32_t first_rows,
+                                                                     int32_t last_rows, EvictPlan* plan, int32_t* list,
+                                                                     int* status) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t sh_prefix, sh_need;
+  __shared__ uint32_t warp_cnt[2][kSelectThreads / 32];
+  const int32_t b = blockIdx.x / c.n_kv;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int32_t len = shown_rows(c, b, 0, status, tid == 0);
+  const int32_t nb = (len + c.block - 1) / c.block;
+  // fixed blocks: [0, head) and [tail, nb)
+  const int32_t head = min(nb, (int32_t)(((int64_t)first_rows + c.block - 1) / c.block));
+  const int32_t tail = max(head, min(nb, (len - min(len, last_rows)) / c.block));
+  const int32_t n_fixed = nb - (tail - head);
+  const int32_t count = min(nb, max(keep, n_fixed));
+  const float* w = weight + (int64_t)blockIdx.x * c.n_blocks;
+  int32_t* out = list + (int64_t)blockIdx.x * c.n_blocks;
+  if (tid == 0 && blockIdx.x % c.n_kv == 0) plan[b] = EvictPlan{len, nb, count, 0};
+
+  // threshold: the (count - n_fixed)-th largest key of [head, tail)
+  uint32_t prefix = 0, need = (uint32_t)(count - n_fixed);
+  const bool all = (int32_t)need >= tail - head;
+  if (!all && need > 0) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
+      __syncthreads();
+      const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
+      for (int32_t j = head + tid; j < tail; j += kSelectThreads) {
+        const uint32_t k = weight_key(w[j]);
+        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      }
+      __syncthreads();
+      if (wid == 0) {  // lane l holds digits 255 - 8l .. 248 - 8l, the largest first
+        uint32_t d[8], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += d[i] = hist[255 - 8 * lane - i];
+        uint32_t before = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const uint32_t t = __shfl_up_sync(0xffffffffu, before, off);
+          if (lane >= off) before += t;
+        }
+        before -= sum;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (before < need && need <= before + d[i]) {
+            sh_prefix = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
+            sh_need = need - before;
+          }
+          before += d[i];
+        }
+      }
+      __syncthreads();
+      prefix = sh_prefix;
+      need = sh_need;
+      __syncthreads();
+    }
+  }
+  // kept blocks in index order
+  uint32_t kept = 0, ties = 0;
+  for (int32_t j0 = 0; j0 < nb; j0 += kSelectThreads) {
+    const int32_t j = j0 + tid;
+    bool sure = j < nb && (j < head || j >= tail || all), tie = false;
+    if (j < nb && !sure && count > n_fixed) {
+      const uint32_t k = weight_key(w[j]);
+      sure = k > prefix;
+      tie = k == prefix;
+    }
+    const uint32_t tie_votes = __ballot_sync(0xffffffffu, tie);
+    if (lane == 0) warp_cnt[0][wid] = __popc(tie_votes);
+    __syncthreads();
+    uint32_t rank = ties, total = ties;
+    for (int i = 0; i < kSelectThreads / 32; ++i) {
+      if (i < wid) rank += warp_cnt[0][i];
+      total += warp_cnt[0][i];
+    }
+    ties = total;
+    rank += __popc(tie_votes & ((1u << lane) - 1u));
+    const bool stay = sure || (tie && rank < need);
+    const uint32_t votes = __ballot_sync(0xffffffffu, stay);
+    if (lane == 0) warp_cnt[1][wid] = __popc(votes);
+    __syncthreads();
+    uint32_t at = kept;
+    total = kept;
+    for (int i = 0; i < kSelectThreads / 32; ++i) {
+      if (i < wid) at += warp_cnt[1][i];
+      total += warp_cnt[1][i];
+    }
+    kept = total;
+    at += __popc(votes & ((1u << lane) - 1u));
+    if (stay && dcheck((int32_t)at < count, status, kWhereKv8Store)) out[at] = j;
+  }
+}
+
+// Blocks move towards the front: the source of the j-th kept block is list[j]
+// >= j, ascending.  A thread owns one 16-byte piece of one row of every block
+// and walks j upwards; it reads list[j + 1], ... before it writes block j, and
+// no later source is a block that it has written, so the move is in place
+// without any thread waiting for another.  Slice z = 2 moves the scales and the
+// weights in the same order and writes the length.
+constexpr int kMoveAhead = 8;
+
+__global__ void __launch_bounds__(256) evict_move_kernel(const Cache c, const EvictPlan* __restrict__ plan,
+                                                         const int32_t* __restrict__ list, const float* weight,
+                                                         float* weight_out, int32_t* lens_out, int* status) {
+  pdl_trigger();
+  pdl_wait();
+  const int32_t b = blockIdx.y / c.n_kv, g = blockIdx.y % c.n_kv;
+  const EvictPlan pl = plan[b];
+  const int32_t* src = list + (int64_t)blockIdx.y * c.n_blocks;
+  if (blockIdx.z == 2) {
+    if (blockIdx.x != 0) return;
+    const int64_t base = (int64_t)blockIdx.y * c.n_blocks;
+    for (int32_t j0 = 0; j0 < pl.count; j0 += (int32_t)blockDim.x) {
+      const int32_t j = j0 + (int32_t)threadIdx.x;
+      float ks = 0.f, vs = 0.f, w = 0.f;
+      if (j < pl.count) {
+        const int32_t s = src[j];
+        ks = c.k_scale[base + s];
+        vs = c.v_scale[base + s];
+        w = weight[base + s];
+      }
+      __syncthreads();
+      if (j < pl.count && dcheck(j < c.n_blocks, status, kWhereKv8Store)) {
+        c.k_scale[base + j] = ks;
+        c.v_scale[base + j] = vs;
+        weight_out[base + j] = w;
+      }
+    }
+    __syncthreads();
+    for (int32_t j = pl.count + (int32_t)threadIdx.x; j < c.n_blocks; j += (int32_t)blockDim.x) {
+      if (j < pl.nb)
+        weight_out[base + j] = 0.f;  // blocks that a later store begins anew
+      else if (weight_out != weight)
+        weight_out[base + j] = weight[base + j];
+    }
+    if (g == 0 && threadIdx.x == 0)
+      lens_out[b] = pl.nb == 0 ? 0 : (pl.count - 1) * c.block + (pl.len - (pl.nb - 1) * c.block);
+    return;
+  }
+  const int per_row = c.hd >> 4;
+  const int unit = (int)blockIdx.x * (int)blockDim.x + (int)threadIdx.x;
+  const int32_t r = unit / per_row;
+  if (r >= c.block) return;
+  uint8_t* base = (blockIdx.z ? c.v : c.k) + ((int64_t)b * c.bstride + r) * c.ld + (int64_t)g * c.hd +
+                  (unit % per_row) * 16;
+  const int64_t step = (int64_t)c.block * c.ld;
+  // blocks before the first one that went stay where they are: find it by bisection (list[j] - j never falls)
+  int32_t lo = 0, hi = pl.count;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (src[mid] > mid)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  for (int32_t j = lo; j < pl.count; j += kMoveAhead) {
+    uint4 x[kMoveAhead];
+    bool live[kMoveAhead];
+#pragma unroll
+    for (int i = 0; i < kMoveAhead; ++i) {
+      live[i] = false;
+      if (j + i < pl.count) {
+        const int32_t s = src[j + i];
+        live[i] = s * c.block + r < pl.len;
+        if (live[i]) x[i] = *reinterpret_cast<const uint4*>(base + s * step);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kMoveAhead; ++i)
+      if (live[i]) *reinterpret_cast<uint4*>(base + (j + i) * step) = x[i];
+  }
+}
+
+// ------------------------------------------------------------------ host
+cosmot_status make_cache(const cosmot_kv8_cache* c, Cache& o) {
+  if (!c) return COSMOT_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return COSMOT_ERR_UNSUPPORTED;
+  if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) return COSMOT_ERR_UNSUPPORTED;
+  if (c->batch < 1 || c->capacity < 1 || c->n_kv_heads < 1) return COSMOT_ERR_INVALID_ARG;
+  if (c->ld < (int64_t)c->n_kv_heads * c->head_dim || c->ld % 16) return COSMOT_ERR_INVALID_ARG;
+  if (c->batch > 1 && c->batch_stride < c->capacity) return COSMOT_ERR_INVALID_ARG;
+  if ((int64_t)c->batch * c->n_kv_heads > 65535) return COSMOT_ERR_UNSUPPORTED;
+  // row indices of the key tiles are 32 bits wide
+  if (c->capacity > INT32_MAX - 256 ||
+      (c->batch > 1 && c->batch_stride > (INT32_MAX - 256 - (int64_t)c->capacity) / (c->batch - 1)))
+    return COSMOT_ERR_UNSUPPORTED;
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->lens) return COSMOT_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v)) return COSMOT_ERR_INVALID_ARG;
+  o = Cache{};
+  o.k = static_cast<uint8_t*>(c->k);
+  o.v = static_cast<uint8_t*>(c->v);
+  o.k_scale = c->k_scale;
+  o.v_scale = c->v_scale;
+  o.lens = c->lens;
+  o.ld = c->ld;
+  o.bstride = c->batch > 1 ? c->batch_stride : 0;
+  o.batch = c->batch;
+  o.capacity = c->capacity;
+  o.n_kv = c->n_kv_heads;
+  o.hd = c->head_dim;
+  o.block = c->block;
+  o.n_blocks = (c->capacity + c->block - 1) / c->block;
+  return COSMOT_OK;
+}
+
+cosmot_status make_query(const cosmot_kv8_cache* c, const cosmot_kv8_query* d, Query& o) {
+  if (!c || !d) return COSMOT_ERR_INVALID_ARG;
+  if (d->n_heads < 1 || c->n_kv_heads < 1 || d->n_heads % c->n_kv_heads) return COSMOT_ERR_INVALID_ARG;
+  if (d->n_q < 0 || d->n_new < 0 || d->n_new > c->capacity || d->max_len < 0) return COSMOT_ERR_INVALID_ARG;
+  if (d->mask_mode != COSMOT_KV8_FULL && d->mask_mode != COSMOT_KV8_CAUSAL) return COSMOT_ERR_INVALID_ARG;
+  if (c->batch > 1 && (d->q_batch_stride < d->n_q || d->o_batch_stride < d->n_q)) return COSMOT_ERR_INVALID_ARG;
+  if (!(d->softmax_scale >= 0.f) || d->softmax_scale > 1e30f) return COSMOT_ERR_INVALID_ARG;
+  o = Query{};
+  o.n_q = d->n_q;
+  o.group = d->n_heads / c->n_kv_heads;
+  o.n_rows = d->n_q * o.group;
+  if (d->n_q > INT32_MAX / 2 / o.group) return COSMOT_ERR_UNSUPPORTED;
+  o.n_heads = d->n_heads;
+  o.n_new = d->n_new;
+  o.causal = d->mask_mode == COSMOT_KV8_CAUSAL;
+  o.q_bstride = c->batch > 1 ? d->q_batch_stride : 0;
+  o.o_bstride = c->batch > 1 ? d->o_batch_stride : 0;
+  o.scale_log2 = (d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / sqrtf((float)c->head_dim)) * kLog2e;
+  o.splits = 1;
+  return COSMOT_OK;
+}
+
+namespace {
+
+// Rows that the host may take any sequence to show (it sizes splits only).
+int32_t bound_len(const cosmot_kv8_cache* c, const cosmot_kv8_query* d) {
+  return d->max_len > 0 && d->max_len < c->capacity ? d->max_len : c->capacity;
+}
+
+cosmot_status check_q(const cosmot_kv8_cache* c, const cosmot_kv8_query* d, const void* q, int64_t ld_q) {
+  if (!q || !aligned16(q) || ld_q % 8 || ld_q < (int64_t)d->n_heads * c->head_dim) return COSMOT_ERR_INVALID_ARG;
+  return COSMOT_OK;
+}
+
+size_t o_part_bytes(const Cache& c, const Query& p) {
+  return ((size_t)p.splits * c.batch * c.n_kv * p.n_rows * c.hd * 4 + 255) & ~size_t(255);
+}
+size_t part_bytes(const Cache& c, const Query& p) {
+  return p.splits == 1 ? 0 : o_part_bytes(c, p) + (size_t)p.splits * c.batch * c.n_kv * p.n_rows * 8;
+}
+
+size_t evict_list_offset(int32_t batch) { return ((size_t)batch * sizeof(EvictPlan) + 255) & ~size_t(255); }
+
+}  // namespace
+}  // namespace kv8
+}  // namespace cosmot
+
+using namespace cosmot;
+
+extern "C" cosmot_status cosmot_kv8_store(const cosmot_kv8_cache* cache, const void* k, const void* v, int64_t ld_src,
+                                          int64_t src_batch_stride, int32_t n_rows, cosmot_stream_t stream) {
+  kv8::Cache c;
+  cosmot_status st = kv8::make_cache(cache, c);
+  if (st != COSMOT_OK) return st;
+  if (!k || !v || !aligned16(k) || !aligned16(v) || ld_src % 8 || ld_src < (int64_t)c.n_kv * c.hd)
+    return COSMOT_ERR_INVALID_ARG;
+  if (n_rows < 0 || n_rows > c.capacity || (c.batch > 1 && src_batch_stride < n_rows)) return COSMOT_ERR_INVALID_ARG;
+  if (n_rows == 0) return COSMOT_OK;
+  int* status = device_status_ptr();
+  if (!status) return COSMOT_ERR_CUDA;
+  const int units = c.block * c.hd / 16;  // 64 .. 1024
+  const dim3 grid((unsigned)(((int64_t)n_rows + 2 * c.block - 2) / c.block), (unsigned)(c.batch * c.n_kv), 2);
+  const dim3 block((unsigned)(units < 256 ? units : 256));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t bs = c.batch > 1 ? src_batch_stride : 0;
+  const auto* ks = static_cast<const __nv_bfloat16*>(k);
+  const auto* vs = static_cast<const __nv_bfloat16*>(v);
+  cudaError_t e;
+  if (units <= 256)
+    e = launch_pdl(kv8::store_kernel<1>, grid, block, 0, s, nullptr, c, ks, vs, ld_src, bs, n_rows, status);
+  else if (units == 512)
+    e = launch_pdl(kv8::store_kernel<2>, grid, block, 0, s, nullptr, c, ks, vs, ld_src, bs, n_rows, status);
+  else
+    e = launch_pdl(kv8::store_kernel<4>, grid, block, 0, s, nullptr, c, ks, vs, ld_src, bs, n_rows, status);
+  return launch_status(e);
+}
+
+extern "C" cosmot_status cosmot_kv8_attention_workspace(const cosmot_kv8_cache* cache, const cosmot_kv8_query* query,
+                                                        size_t* bytes) {
+  kv8::Cache c;
+  kv8::Query p;
+  if (!bytes) return COSMOT_ERR_INVALID_ARG;
+  cosmot_status st = kv8::make_cache(cache, c);
+  if (st == COSMOT_OK) st = kv8::make_query(cache, query, p);
+  if (st != COSMOT_OK) return st;
+  p.splits = kv8::rows_splits(c, p, kv8::bound_len(cache, query));
+  *bytes = kv8::part_bytes(c, p);
+  return COSMOT_OK;
+}
+
+extern "C" cosmot_status cosmot_kv8_attention(const cosmot_kv8_cache* cache, const cosmot_kv8_query* query,
+                                              const void* q, int64_t ld_q, void* o, int64_t ld_o, float* lse,
+                                              void* workspace, size_t workspace_bytes, cosmot_stream_t stream) {
+  kv8::Cache c;
+  kv8::Query p;
+  cosmot_status st = kv8::make_cache(cache, c);
+  if (st == COSMOT_OK) st = kv8::make_query(cache, query, p);
+  if (st == COSMOT_OK) st = kv8::check_q(cache, query, q, ld_q);
+  if (st != COSMOT_OK) return st;
+  if (!o || !aligned16(o) || ld_o % 8 || ld_o < (int64_t)p.n_heads * c.hd) return COSMOT_ERR_INVALID_ARG;
+  p.splits = kv8::rows_splits(c, p, kv8::bound_len(cache, query));
+  if (p.splits > 1) {
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return COSMOT_ERR_INVALID_ARG;
+    if (workspace_bytes < kv8::part_bytes(c, p)) return COSMOT_ERR_WORKSPACE;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kv8::o_part_bytes(c, p));
+  }
+  if (p.n_q == 0) return COSMOT_OK;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.ld_q = ld_q;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.ld_o = ld_o;
+  p.lse = lse;
+  p.status = device_status_ptr();
+  if (!p.status) return COSMOT_ERR_CUDA;
+  return kv8::rows_attention(c, p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" cosmot_status cosmot_kv8_weigh(const cosmot_kv8_cache* cache, const cosmot_kv8_query* query, const void* q,
+                                          int64_t ld_q, const float* lse, float decay, float* weight,
+                                          cosmot_stream_t stream) {
+  kv8::Cache c;
+  kv8::Query p;
+  cosmot_status st = kv8::make_cache(cache, c);
+  if (st == COSMOT_OK) st = kv8::make_query(cache, query, p);
+  if (st == COSMOT_OK) st = kv8::check_q(cache, query, q, ld_q);
+  if (st != COSMOT_OK) return st;
+  if (!lse || !weight || !(decay >= 0.f) || decay > 1e30f) return COSMOT_ERR_INVALID_ARG;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.ld_q = ld_q;
+  p.lse = const_cast<float*>(lse);
+  p.status = device_status_ptr();
+  if (!p.status) return COSMOT_ERR_CUDA;
+  return kv8::rows_weigh(c, p, decay, weight, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" cosmot_status cosmot_kv8_evict_workspace(const cosmot_kv8_cache* cache, size_t* bytes) {
+  kv8::Cache c;
+  if (!bytes) return COSMOT_ERR_INVALID_ARG;
+  const cosmot_status st = kv8::make_cache(cache, c);
+  if (st != COSMOT_OK) return st;
+  *bytes = kv8::evict_list_offset(c.batch) + (size_t)c.batch * c.n_kv * c.n_blocks * sizeof(int32_t);
+  return COSMOT_OK;
+}
+
+extern "C" cosmot_status cosmot_kv8_evict(const cosmot_kv8_cache* cache, const float* weight, int32_t keep_blocks,
+                                          int32_t first_rows, int32_t last_rows, float* weight_out, int32_t* lens_out,
+                                          void* workspace, size_t workspace_bytes, cosmot_stream_t stream) {
+  kv8::Cache c;
+  cosmot_status st = kv8::make_cache(cache, c);
+  if (st != COSMOT_OK) return st;
+  if (!weight || !weight_out || !lens_out || keep_blocks < 1 || first_rows < 0 || last_rows < 0)
+    return COSMOT_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return COSMOT_ERR_INVALID_ARG;
+  size_t need = 0;
+  if (cosmot_kv8_evict_workspace(cache, &need) != COSMOT_OK || workspace_bytes < need) return COSMOT_ERR_WORKSPACE;
+  int* status = device_status_ptr();
+  if (!status) return COSMOT_ERR_CUDA;
+  auto* plan = static_cast<kv8::EvictPlan*>(workspace);
+  auto* list = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kv8::evict_list_offset(c.batch));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = launch_status(launch_pdl(kv8::evict_select_kernel, dim3((unsigned)(c.batch * c.n_kv)),
+                                dim3(kv8::kSelectThreads), 0, s, nullptr, c, weight, keep_blocks, first_rows, last_rows,
+                                plan, list, status));
+  if (st != COSMOT_OK) return st;
+  const unsigned slices = (unsigned)((c.block * c.hd / 16 + 255) / 256);
+  return launch_status(launch_pdl(kv8::evict_move_kernel, dim3(slices, (unsigned)(c.batch * c.n_kv), 3), dim3(256), 0, s,
+                                  nullptr, c, (const kv8::EvictPlan*)plan, (const int32_t*)list, weight, weight_out,
+                                  lens_out, status));
+}

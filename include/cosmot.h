@@ -57,7 +57,8 @@ enum {
   COSMOT_ERR_CUDA = 3,
   COSMOT_ERR_TIMEOUT = 4,
   COSMOT_ERR_WORKSPACE = 5,
-  COSMOT_ERR_BOUNDS = 6     /* debug build only: a device-side store index check failed (store skipped) */
+  COSMOT_ERR_BOUNDS = 6     /* a device-side store index check failed (debug build; store skipped), or a length of
+                               an 8-bit cache lies outside its capacity (either build; see cosmot_kv8_cache) */
 };
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -358,6 +359,127 @@ COSMOT_API cosmot_status cosmot_flow_cfg_euler_step(void* x_cond, void* x_base, 
                                                     const void* v_base, int64_t ld_v, int64_t n_rows, int64_t n_cols,
                                                     double sigma, double sigma_next, double guidance,
                                                     cosmot_stream_t stream);
+
+/* ===================================================================== 8-bit key/value cache */
+
+/*
+ * A key/value cache in 8 bits for long streaming histories ("流式生成如何工作":
+ * finished blocks stay in the cache) and for many sequences: e4m3 bytes with one
+ * float32 scale for each block of `block` rows and head, keys and values apart,
+ *     K[b][r][g][:] = k[b][r][g][:] * k_scale[b][g][r / block]   (V likewise),
+ * g a key/value head.  Keys are stored rotated by mRoPE, as in the workspace's
+ * bf16 cache, so rows may be dropped without touching the others.
+ *   k, v     device e4m3 [batch][batch_stride rows][ld], heads of head_dim from
+ *            element 0; 16-byte aligned, ld a multiple of 16
+ *   k_scale, v_scale  device float32 [batch][n_kv_heads][ceil(capacity / block)];
+ *            positive, and those of values within [2^-40, 2^40] (what
+ *            cosmot_kv8_store writes)
+ *   lens     device int32 [batch]: rows that each sequence holds, [0, capacity].
+ *            The kernels read it, so a captured graph follows it.  A value
+ *            outside (or without room for the rows of the call) latches
+ *            COSMOT_ERR_BOUNDS; nothing is read or written out of place: a store
+ *            then writes none of that sequence's rows, the other calls take the
+ *            nearest length inside.
+ * head_dim 64 or 128, block 16, 32, 64 or 128 (else UNSUPPORTED); any capacity.
+ * Contents of rows at and behind lens (+ n_new) are never read.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* lens;
+  int64_t ld;           /* elements between rows, >= n_kv_heads * head_dim */
+  int64_t batch_stride; /* rows between sequences, >= capacity (batch > 1) */
+  int32_t batch, capacity;
+  int32_t n_kv_heads, head_dim;
+  int32_t block;
+  int32_t reserved;
+} cosmot_kv8_cache;
+
+/*
+ * Stores n_rows rows behind the ones each sequence holds: input row i of
+ * sequence b becomes row lens[b] + i (lens itself is the caller's to advance, so
+ * a denoising step may store its block's rows anew).  k, v: device bf16
+ * [batch][src_batch_stride rows][ld_src], 16-byte aligned, ld_src % 8 == 0; the
+ * K and V columns of a QKV projection fit as they are.
+ * A block's scale is 2^e, e the smallest in [-40, 40] with its largest finite
+ * magnitude <= 448 * 2^e; elements are x / scale to nearest even, saturating
+ * (infinities too; NaN stays NaN).  A power of two costs e4m3 no precision and
+ * makes rescaling exact.  Where the first block holds rows already, its scale
+ * never shrinks, and if it grows those rows are rounded again.  Rows at and
+ * behind lens[b] + n_rows keep their bytes, but those of the last block written
+ * may get another scale.
+ */
+COSMOT_API cosmot_status cosmot_kv8_store(const cosmot_kv8_cache* cache, const void* k, const void* v, int64_t ld_src,
+                                          int64_t src_batch_stride, int32_t n_rows, cosmot_stream_t stream);
+
+/* Key visibility over a cache that shows L = lens[b] + n_new rows: FULL, every
+ * query sees all of them (DM rows); CAUSAL, query i is row L - n_q + i and sees
+ * the rows up to itself (AR rows; none where that row is negative). */
+enum { COSMOT_KV8_FULL = 0, COSMOT_KV8_CAUSAL = 1 };
+
+typedef struct {
+  int64_t n_q;            /* queries of each sequence */
+  int64_t q_batch_stride; /* rows between sequences of q, >= n_q (batch > 1) */
+  int64_t o_batch_stride; /* the same of o (attention only; >= n_q) */
+  int32_t n_heads;        /* query heads, a multiple of the cache's n_kv_heads */
+  int32_t n_new;          /* rows behind lens[b] that count as well: stored, not yet advanced over */
+  int32_t mask_mode;      /* COSMOT_KV8_* */
+  int32_t max_len;        /* the most rows any sequence shows, 0 = capacity: sizes the split of the keys
+                             only, results are right for longer sequences too */
+  float softmax_scale;    /* 0 = 1/sqrt(head_dim) */
+  int32_t reserved;
+} cosmot_kv8_query;
+
+/*
+ * Attention over the 8-bit cache: per head h (key head h / (n_heads / n_kv_heads))
+ *     o_i = sum_{j visible to i} softmax_j(q_i . K_j * scale) V_j
+ * q: device bf16 [batch][q_batch_stride][ld_q], o the same with ld_o, both
+ * 16-byte aligned with ld % 8 == 0.  lse: NULL, or device float32
+ * [batch][n_heads][n_q], the natural logarithm of each softmax's sum.  A row
+ * that sees nothing gives 0 and -infinity.  A query row with a NaN or an
+ * infinity gives NaN; a NaN among a sequence's shown keys or values may reach
+ * all of its queries.  workspace: cosmot_kv8_attention_workspace bytes
+ * (256-byte aligned, may be NULL when that is 0), for this call alone: calls
+ * that may run at the same time need their own.
+ */
+COSMOT_API cosmot_status cosmot_kv8_attention_workspace(const cosmot_kv8_cache* cache, const cosmot_kv8_query* query,
+                                                        size_t* bytes);
+COSMOT_API cosmot_status cosmot_kv8_attention(const cosmot_kv8_cache* cache, const cosmot_kv8_query* query,
+                                              const void* q, int64_t ld_q, void* o, int64_t ld_o, float* lse,
+                                              void* workspace, size_t workspace_bytes, cosmot_stream_t stream);
+
+/*
+ * Accumulates the attention weight that each block of rows receives:
+ *     weight[b][g][j] = decay * weight[b][g][j]
+ *         + sum_{rows r of block j} sum_{heads h of g} sum_{queries i that see r} exp(q_i . K_r * scale - lse[b][h][i])
+ * for the blocks that hold a shown row; the others are left as they are.
+ * weight: device float32 [batch][n_kv_heads][ceil(capacity / block)]; lse as
+ * cosmot_kv8_attention wrote it for the same query (rows of -infinity add
+ * nothing).  decay >= 0.
+ */
+COSMOT_API cosmot_status cosmot_kv8_weigh(const cosmot_kv8_cache* cache, const cosmot_kv8_query* query, const void* q,
+                                          int64_t ld_q, const float* lse, float decay, float* weight,
+                                          cosmot_stream_t stream);
+
+/*
+ * Eviction by accumulated weight, for every sequence and key head apart: of the
+ * ceil(lens[b] / block) blocks, keep_blocks (>= 1) stay: first those that hold one
+ * of the first first_rows or the last last_rows rows, or only a part of a block
+ * (all of them, even if more than keep_blocks), then those of the most weight,
+ * the lower index first among equals (NaN counts as more than infinity).  The
+ * rows of the blocks that stay move up in order, in place, with their scales and
+ * weights.  weight_out receives the moved weights, 0 for the blocks that were
+ * given up, and elsewhere weight's values; it may be weight itself.  lens_out
+ * receives the new lengths and may be the cache's lens.  Cached rows at and
+ * behind the new length keep their bytes.  workspace: 256-byte aligned,
+ * cosmot_kv8_evict_workspace bytes, for this call alone.
+ */
+COSMOT_API cosmot_status cosmot_kv8_evict_workspace(const cosmot_kv8_cache* cache, size_t* bytes);
+COSMOT_API cosmot_status cosmot_kv8_evict(const cosmot_kv8_cache* cache, const float* weight, int32_t keep_blocks,
+                                          int32_t first_rows, int32_t last_rows, float* weight_out, int32_t* lens_out,
+                                          void* workspace, size_t workspace_bytes, cosmot_stream_t stream);
 
 /* ===================================================================== layer */
 
