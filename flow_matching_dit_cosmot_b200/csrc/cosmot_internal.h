@@ -28,6 +28,10 @@ enum Where : int {
   // 8-bit cache: a length outside its capacity, and the debug build's store checks
   kWhereKv8Lens = 400,
   kWhereKv8Store = 401,
+  kWhereKv8Mma = 402,
+  kWhereKv8Softmax = 403,
+  kWhereKv8Widen = 404,
+  kWhereKv8Drain = 405,
   kWhereSelftest = COSMOT_SITE_SELFTEST,
   kWhereSelftestBounds = COSMOT_SITE_SELFTEST_BOUNDS,
 };
@@ -37,6 +41,12 @@ enum Where : int {
 // 128-byte swizzle), out-of-bounds elements read as zero.
 cosmot_status make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,
                                 uint32_t box_rows, uint32_t box_cols);
+
+// The same of [d3][d2][d1][d0] elements: d1 rows of d0 side by side, `ld`
+// elements from one d2 to the next and `ld3` of those from one d3 to the next;
+// box of 1 x box2 x box1 x box0 (box0 * 2 == 128 bytes).
+cosmot_status make_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3,
+                                uint64_t ld, uint64_t ld3, uint32_t box0, uint32_t box1, uint32_t box2);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -370,6 +370,10 @@ size_t part_bytes(const Cache& c, const Query& p) {
   return p.splits == 1 ? 0 : o_part_bytes(c, p) + (size_t)p.splits * c.batch * c.n_kv * p.n_rows * 8;
 }
 
+// Up to kRowsMax packed rows the register-tile kernels run, above it the tcgen05 ones.
+constexpr int64_t kRowsMax = 32;
+bool use_tiles(const Query& p) { return p.n_rows > kRowsMax; }
+
 size_t evict_list_offset(int32_t batch) { return ((size_t)batch * sizeof(EvictPlan) + 255) & ~size_t(255); }
 
 }  // namespace
@@ -414,6 +418,10 @@ extern "C" cosmot_status cosmot_kv8_attention_workspace(const cosmot_kv8_cache* 
   cosmot_status st = kv8::make_cache(cache, c);
   if (st == COSMOT_OK) st = kv8::make_query(cache, query, p);
   if (st != COSMOT_OK) return st;
+  if (kv8::use_tiles(p)) {
+    *bytes = kv8::tile_workspace(c, p, kv8::bound_len(cache, query));
+    return COSMOT_OK;
+  }
   p.splits = kv8::rows_splits(c, p, kv8::bound_len(cache, query));
   *bytes = kv8::part_bytes(c, p);
   return COSMOT_OK;
@@ -429,10 +437,15 @@ extern "C" cosmot_status cosmot_kv8_attention(const cosmot_kv8_cache* cache, con
   if (st == COSMOT_OK) st = kv8::check_q(cache, query, q, ld_q);
   if (st != COSMOT_OK) return st;
   if (!o || !aligned16(o) || ld_o % 8 || ld_o < (int64_t)p.n_heads * c.hd) return COSMOT_ERR_INVALID_ARG;
-  p.splits = kv8::rows_splits(c, p, kv8::bound_len(cache, query));
-  if (p.splits > 1) {
+  const int32_t max_len = kv8::bound_len(cache, query);
+  const bool tiles = kv8::use_tiles(p);
+  if (!tiles) p.splits = kv8::rows_splits(c, p, max_len);
+  const size_t need = tiles ? kv8::tile_workspace(c, p, max_len) : kv8::part_bytes(c, p);
+  if (need > 0) {
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return COSMOT_ERR_INVALID_ARG;
-    if (workspace_bytes < kv8::part_bytes(c, p)) return COSMOT_ERR_WORKSPACE;
+    if (workspace_bytes < need) return COSMOT_ERR_WORKSPACE;
+  }
+  if (!tiles && need > 0) {
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kv8::o_part_bytes(c, p));
   }
@@ -444,7 +457,8 @@ extern "C" cosmot_status cosmot_kv8_attention(const cosmot_kv8_cache* cache, con
   p.lse = lse;
   p.status = device_status_ptr();
   if (!p.status) return COSMOT_ERR_CUDA;
-  return kv8::rows_attention(c, p, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return tiles ? kv8::tile_attention(c, p, max_len, workspace, s) : kv8::rows_attention(c, p, s);
 }
 
 extern "C" cosmot_status cosmot_kv8_weigh(const cosmot_kv8_cache* cache, const cosmot_kv8_query* query, const void* q,
@@ -462,7 +476,10 @@ extern "C" cosmot_status cosmot_kv8_weigh(const cosmot_kv8_cache* cache, const c
   p.lse = const_cast<float*>(lse);
   p.status = device_status_ptr();
   if (!p.status) return COSMOT_ERR_CUDA;
-  return kv8::rows_weigh(c, p, decay, weight, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return kv8::use_tiles(p) && p.group <= 128
+             ? kv8::tile_weigh(c, p, decay, weight, kv8::bound_len(cache, query), s)
+             : kv8::rows_weigh(c, p, decay, weight, s);
 }
 
 extern "C" cosmot_status cosmot_kv8_evict_workspace(const cosmot_kv8_cache* cache, size_t* bytes) {

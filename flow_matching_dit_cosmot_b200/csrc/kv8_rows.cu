@@ -31,11 +31,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // One row's 16-dim pieces for this lane (its j), scaled into f16; returns the
 // factor that takes the scaled scores back (NaN for a row that is not finite).
 template <int HD>
@@ -132,15 +127,6 @@ __device__ __forceinline__ void load_q_tile(const Cache& c, const Query& p, int3
         q[m][k][2 + i] = f[k][1];
       }
     }
-}
-
-__device__ __forceinline__ void store_o8(__nv_bfloat16* dst, const float* v) {
-  uint4 x;
-  x.x = pack_bf16x2(v[0], v[1]);
-  x.y = pack_bf16x2(v[2], v[3]);
-  x.z = pack_bf16x2(v[4], v[5]);
-  x.w = pack_bf16x2(v[6], v[7]);
-  *reinterpret_cast<uint4*>(dst) = x;
 }
 
 // ------------------------------------------------------------------ attention
@@ -305,7 +291,7 @@ __global__ void __launch_bounds__(32 * kWarps) rows_attention_kernel(const Cache
       float4* dst = reinterpret_cast<float4*>(p.part_o + pr * HD + col);
       dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
       dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-      if (col == 0) p.part_ml[pr] = make_float2(m, lsum);
+      if (col == 0) p.part_ml[pr] = make_float2(lsum == 0.f ? -INFINITY : m - kPBias, lsum);
     } else {
       const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
 #pragma unroll
@@ -331,35 +317,15 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const Cache c, const Que
   if (u >= rows * (HD / 8)) return;
   const int64_t pr = u / (HD / 8);
   const int col = (int)(u % (HD / 8)) * 8;
-  float m = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.part_ml[s * rows + pr].x);
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, lsum = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = p.part_ml[s * rows + pr];
-    const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - m);
-    lsum = fmaf(f, ml.y, lsum);
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + (s * rows + pr) * HD + col);
-    const float4 x = src[0], y = src[1];
-    acc[0] = fmaf(f, x.x, acc[0]);
-    acc[1] = fmaf(f, x.y, acc[1]);
-    acc[2] = fmaf(f, x.z, acc[2]);
-    acc[3] = fmaf(f, x.w, acc[3]);
-    acc[4] = fmaf(f, y.x, acc[4]);
-    acc[5] = fmaf(f, y.y, acc[5]);
-    acc[6] = fmaf(f, y.z, acc[6]);
-    acc[7] = fmaf(f, y.w, acc[7]);
-  }
-  const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] *= inv;
+  float acc[8], lse;
+  join_row<HD>(p.part_o, p.part_ml, p.splits, rows, pr, col, acc, lse);
   const int64_t bg = pr / p.n_rows, r = pr % p.n_rows;
   const int32_t b = (int32_t)(bg / c.n_kv), kvh = (int32_t)(bg % c.n_kv);
   const int64_t qi = r / p.group;
   const int32_t h = kvh * p.group + (int32_t)(r % p.group);
   if (!dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store)) return;
   store_o8(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col, acc);
-  if (col == 0 && p.lse)
-    p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = lsum == 0.f ? -INFINITY : (m - kPBias + log2f(lsum)) * kLn2;
+  if (col == 0 && p.lse) p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = lse;
 }
 
 // ------------------------------------------------------------------ weighing

@@ -1,0 +1,897 @@
+// Attention and weighing over the 8-bit cache for many query rows, on the
+// tcgen05 tensor cores (TMEM accumulators).
+//
+// Attention.  One CTA per (sequence, key head, 256 packed query rows) and, for
+// the items of the last wave, per key split.  512 threads in four warpgroups:
+//   warp 0       owns TMEM and issues the MMAs from one thread:
+//                  S_t = Q_t K_j^T   (M 128, N 128, K head_dim; both in smem)
+//                  O_t += P_t V_j    (A = P in TMEM over S)
+//                in the order S0 S1 | PV0 S0' PV1 S1' | ..., so that one tile's
+//                products run beside the other tile's softmax.
+//   warps 4-7    read the cache's bytes (16 a load), widen them to f16 (exact)
+//                and write the 128-byte-swizzled tiles that the MMAs read, one
+//                K or V tile ahead in registers and four slots ahead in smem.
+//   warps 8-11   softmax of rows 0-127, warps 12-15 of rows 128-255, a row per
+//                thread; first they bring their rows of Q into smem as f16, by a
+//                power of two per row (its largest magnitude in [2^13, 2^14):
+//                exact down to 2^-31 of it).
+// The scales of a 128-key tile come as eight groups of 16 keys (block >= 16):
+//     x = s (q factor)(ks) + log2 vs,   p vs = 2^(x - m + 8)  (f16 in TMEM),
+// m the running maximum of x; it is followed only when it grows by more than
+// 2^7, so p vs stays below 2^15 and f16 keeps full precision down to 2^-22 of
+// the largest weight.  l = sum (p vs) / vs stays in float32.
+//
+// Weighing.  One CTA per (sequence, key head, 256 keys): the keys are widened
+// to bf16 once and stay in smem, the queries' tiles come by TMA as they are
+// (bf16), and every thread of four warpgroups owns one query row of a tile:
+// per group of 16 keys it adds 2^(s f - lse).  Nothing but the sums leaves the
+// CTA; a cluster may share the queries of one key range, and the sums are
+// joined in a fixed order.
+#include "kv8.cuh"
+
+#include <mutex>
+
+namespace cosmot {
+namespace kv8 {
+namespace {
+
+constexpr int kTile = 128;                    // rows of a query tile, keys of a key tile
+constexpr int kSlots = 4;
+constexpr int kBoxBytes = 128 * 64 * 2;       // 128 rows x 64 columns of 16 bits, 128-byte swizzle
+constexpr float kTileBias = 8.f;
+constexpr float kFollow = 7.f;                // log2 units
+
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Byte offset of 16-byte piece `piece` (of 8 columns) of `row` in a tile of boxes of 64 columns.
+__device__ __forceinline__ uint32_t sw_offset(int row, int piece) {
+  return (uint32_t)((piece >> 3) * kBoxBytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// ------------------------------------------------------------------ attention
+// Registers: 128 threads x (kRegsMma + kRegsConv) + 256 x kRegsSoftmax must not
+// exceed the launch's pool (the launch checks it).
+constexpr int kAttnThreads = 512;
+constexpr int kRegsMma = 48, kRegsConv = 80, kRegsSoftmax = 192;
+
+struct TilePlan {
+  int32_t pairs;    // pairs of query tiles of a (sequence, key head)
+  int32_t n_full;   // leading items that one CTA takes whole
+  int32_t n_tail;   // the others, `splits` CTAs each
+  int32_t splits;
+};
+
+template <int HD>
+struct AttnCfg {
+  static constexpr int kBoxes = HD / 64;
+  static constexpr int kTileBytes = kTile * HD * 2;
+  static constexpr int kScaleBytes = 4 * 8 * 16;  // four key tiles in flight, eight groups each
+  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 256 + kScaleBytes + 1024;
+  static constexpr uint32_t kIdescS = idesc_f16_f32(kTile, kTile, false);
+  static constexpr uint32_t kIdescO = idesc_f16_f32(kTile, HD, true);
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    tile_attention_kernel(const __grid_constant__ Cache c, const __grid_constant__ Query p,
+                          const __grid_constant__ TilePlan plan) {
+  using C = AttnCfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sQ = smem_u32(smem);
+  const uint32_t sKV = sQ + 2 * C::kTileBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (2 + kSlots) * C::kTileBytes);
+  const uint32_t bar_q = smem_u32(bars);
+  const uint32_t bar_kv_full = bar_q + 8;                 // [kSlots]
+  const uint32_t bar_kv_empty = bar_kv_full + 8 * kSlots; // [kSlots]
+  const uint32_t bar_s_full = bar_kv_empty + 8 * kSlots;  // [2]
+  const uint32_t bar_p_half = bar_s_full + 16;            // [2] P of keys 0-63 written
+  const uint32_t bar_p_full = bar_p_half + 16;            // [2] P of keys 64-127 written
+  const uint32_t bar_o_done = bar_p_full + 16;            // [1]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 1 + 2 * kSlots + 7);
+  float4* scales = reinterpret_cast<float4*>(smem + (2 + kSlots) * C::kTileBytes + 256);  // [4][8] (ks, log2 vs, 1/vs)
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // work item: the pairs of all heads in turn (causal: the longest first)
+  int32_t item = (int32_t)blockIdx.x, split = 0, splits = 1;
+  if (item >= plan.n_full) {
+    split = (item - plan.n_full) % plan.splits;
+    item = plan.n_full + (item - plan.n_full) / plan.splits;
+    splits = plan.splits;
+  }
+  const int32_t heads = c.batch * c.n_kv;
+  const int32_t bg = item % heads, b = bg / c.n_kv, kvh = bg % c.n_kv;
+  const int32_t pair = p.causal ? plan.pairs - 1 - item / heads : item / heads;
+  const int64_t r0 = (int64_t)pair * 2 * kTile;
+  const bool two = r0 + kTile < p.n_rows;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar_q, 8);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(bar_kv_full + 8 * s, 4);
+      mbar_init(bar_kv_empty + 8 * s, 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar_s_full + 8 * t, 1);
+      mbar_init(bar_p_half + 8 * t, 4);
+      mbar_init(bar_p_full + 8 * t, 4);
+    }
+    mbar_init(bar_o_done, 1);
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  // up to here only the CTA's own shared and tensor memory and the parameters were touched
+  pdl_trigger();
+  pdl_wait();
+  const int32_t len = shown_rows(c, b, p.n_new, p.status, threadIdx.x == 0);
+  const int64_t r_end = r0 + 2 * kTile < p.n_rows ? r0 + 2 * kTile : p.n_rows;
+  const int32_t kend = row_limit(p, r_end - 1, len);
+  const int32_t n_kt = (kend + kTile - 1) / kTile;
+  const int32_t kt0 = (int32_t)((int64_t)split * n_kt / splits), kt1 = (int32_t)((int64_t)(split + 1) * n_kt / splits);
+  const int32_t n_vis = kt1 - kt0;  // key tiles of this CTA
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const uint32_t s_col[2] = {0u, 128u}, o_col[2] = {256u, 256u + HD};
+
+  if (warp < 4) {
+    setmaxnreg_dec<kRegsMma>();
+    if (warp == 0 && lane == 0 && n_vis > 0) {
+      auto issue_s = [&](int t, int slot) {
+        const uint32_t qa = sQ + t * C::kTileBytes, ka = sKV + slot * C::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t off = (k >> 2) * kBoxBytes + (k & 3) * 32;
+          umma_ss(tmem_base + s_col[t], sw128_desc(qa + off, 16, 1024), sw128_desc(ka + off, 16, 1024), C::kIdescS,
+                  k > 0 ? 1u : 0u);
+        }
+      };
+      auto issue_pv = [&](int t, int slot, bool acc, int half) {  // keys 64 half .. 64 half + 63
+        const uint32_t va = sKV + slot * C::kTileBytes;
+#pragma unroll
+        for (int k = 4 * half; k < 4 * half + 4; ++k)
+          umma_ts(tmem_base + o_col[t], tmem_base + s_col[t] + 8 * k, sw128_desc(va + 2048 * k, kBoxBytes, 1024),
+                  C::kIdescO, (acc || k > 0) ? 1u : 0u);
+      };
+      auto wait = [&](uint32_t bar, uint32_t par) { return mbar_wait(bar, par, p.status, kWhereKv8Mma); };
+      auto kv_wait = [&](int L) { return wait(bar_kv_full + 8 * (L % kSlots), (L / kSlots) & 1); };
+      bool ok = wait(bar_q, 0) && kv_wait(0);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0, 0);
+        umma_commit(bar_s_full);
+        if (two) {
+          issue_s(1, 0);
+          umma_commit(bar_s_full + 8);
+        }
+        umma_commit(bar_kv_empty);
+      }
+      for (int j = 0; j < n_vis && ok; ++j) {
+        const int LV = 2 * j + 1, LK = 2 * j + 2;
+        const bool has_next = j + 1 < n_vis;
+        const uint32_t par = j & 1;
+        if (!kv_wait(LV) || !wait(bar_p_half, par)) break;
+        tc_fence_after();
+        issue_pv(0, LV % kSlots, j > 0, 0);
+        if (!wait(bar_p_full, par)) break;
+        tc_fence_after();
+        issue_pv(0, LV % kSlots, true, 1);
+        if (has_next) {
+          if (!kv_wait(LK)) break;
+          tc_fence_after();
+          issue_s(0, LK % kSlots);
+          umma_commit(bar_s_full);
+        }
+        if (two) {
+          if (!wait(bar_p_half + 8, par)) break;
+          tc_fence_after();
+          issue_pv(1, LV % kSlots, j > 0, 0);
+          if (!wait(bar_p_full + 8, par)) break;
+          tc_fence_after();
+          issue_pv(1, LV % kSlots, true, 1);
+        }
+        umma_commit(bar_kv_empty + 8 * (LV % kSlots));
+        if (has_next) {
+          if (two) {
+            issue_s(1, LK % kSlots);
+            umma_commit(bar_s_full + 8);
+          }
+          umma_commit(bar_kv_empty + 8 * (LK % kSlots));
+        }
+      }
+      umma_commit(bar_o_done);
+      mbar_wait(bar_o_done, 0, p.status, kWhereKv8Drain);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    setmaxnreg_dec<kRegsConv>();
+    // ---------------------------------------------------------- widening
+    constexpr int kUnits = HD / 16;          // 16-byte pieces of a cached row
+    constexpr int kStep = 128 / kUnits;      // rows of one load of the warpgroup
+    constexpr int kLoads = kTile / kStep;
+    const int ct = (int)threadIdx.x - 128, u = ct % kUnits, row = ct / kUnits;
+    // two pieces of 8 columns; the second box's threads write them in the other order (bank conflicts)
+    const int swap = u >> 2;
+    const uint8_t* src[2] = {c.k + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD + u * 16,
+                             c.v + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD + u * 16};
+    const float* ksp = c.k_scale + (int64_t)bg * c.n_blocks;
+    const float* vsp = c.v_scale + (int64_t)bg * c.n_blocks;
+    uint4 w[kLoads];
+    auto load = [&](int L) {
+      const uint8_t* base = src[L & 1];
+      const int32_t key0 = (kt0 + (L >> 1)) * kTile + row;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (key0 + i * kStep < kend) w[i] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)(key0 + i * kStep) * c.ld));
+      }
+    };
+    if (n_vis > 0) load(0);
+    for (int L = 0; L < 2 * n_vis; ++L) {
+      const int slot = L % kSlots;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar_kv_empty + 8 * slot, ((L / kSlots) & 1) ^ 1, p.status, kWhereKv8Widen)))
+        break;
+      const uint32_t dst = sKV + slot * C::kTileBytes;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = row + i * kStep;
+        const uint32_t a0 = cvt_lo(w[i].x), a1 = cvt_hi(w[i].x), a2 = cvt_lo(w[i].y), a3 = cvt_hi(w[i].y);
+        const uint32_t b0 = cvt_lo(w[i].z), b1 = cvt_hi(w[i].z), b2 = cvt_lo(w[i].w), b3 = cvt_hi(w[i].w);
+        const uint32_t da = dst + sw_offset(r, 2 * u), db = dst + sw_offset(r, 2 * u + 1);
+        if (swap) {
+          st_shared16(db, b0, b1, b2, b3);
+          st_shared16(da, a0, a1, a2, a3);
+        } else {
+          st_shared16(da, a0, a1, a2, a3);
+          st_shared16(db, b0, b1, b2, b3);
+        }
+      }
+      if (!(L & 1) && ct < 8) {  // the key tile's scales, with its keys
+        const int32_t kt = kt0 + (L >> 1), key = kt * kTile + ct * 16;
+        float4 s = make_float4(1.f, 0.f, 0.f, 0.f);  // a group behind the end: finite, and every key masked
+        if (key < kend) {
+          s.x = __ldg(ksp + key / c.block);
+          scale_log2_parts(__ldg(vsp + key / c.block), s.y, s.z);
+        }
+        scales[((L >> 1) & 3) * 8 + ct] = s;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_kv_full + 8 * slot);
+      if (L + 1 < 2 * n_vis) load(L + 1);
+    }
+  } else {
+    setmaxnreg_inc<kRegsSoftmax>();
+    // ---------------------------------------------------------- softmax
+    const int t = (warp - 8) >> 2;           // query tile
+    const int lane_base = (warp & 3) * 32;   // TMEM lanes this warp may access
+    const int64_t r = r0 + t * kTile + lane_base + lane;
+    const bool valid = r < p.n_rows;
+    const int64_t qi = valid ? r / p.group : 0;
+    const int32_t h = kvh * p.group + (int32_t)(valid ? r % p.group : 0);
+    float fac = p.scale_log2;
+    if (n_vis > 0 && (t == 0 || two)) {
+      const uint4* q4 = reinterpret_cast<const uint4*>(p.q + (b * p.q_bstride + qi) * p.ld_q + (int64_t)h * HD);
+      uint4 x[HD / 8];
+      float amax = 0.f;
+      bool finite = true;
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i) {
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (valid) x[i] = __ldg(q4 + i);
+      }
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = unpack_bf16x2(w[e]);
+          amax = fmax3(amax, fabsf(v.x), fabsf(v.y));
+          finite = finite && fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY;
+        }
+      }
+      // below 2^-47 a row loses bits of less than 2^-85: nothing that a key could raise to a visible score
+      int e2 = (int)((__float_as_uint(amax) >> 23) & 255u) - 127 - 13;
+      e2 = e2 < -60 ? -60 : (e2 > 114 ? 114 : e2);
+      const float down = exp2_int(-e2);
+      fac = finite ? fmaxf(p.scale_log2 * exp2_int(e2), 1e-25f) : __int_as_float(0x7fc00000);
+      const uint32_t dst = sQ + t * C::kTileBytes;
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i]);
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = unpack_bf16x2(w[e]);
+          y[e] = pack_f16x2(v.x * down, v.y * down);
+        }
+        st_shared16(dst + sw_offset(lane_base + lane, i), y[0], y[1], y[2], y[3]);
+      }
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_q);
+
+    const uint32_t s_addr = tmem_base + ((uint32_t)lane_base << 16) + s_col[t];
+    const uint32_t o_addr = tmem_base + ((uint32_t)lane_base << 16) + o_col[t];
+    const int32_t lim = valid ? row_limit(p, r, len) : kend;  // padding rows see all: they never force the masks
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    if (t == 0 || two) {
+#pragma unroll 1
+      for (int j = 0; j < n_vis; ++j) {
+        const int32_t kbase = (kt0 + j) * kTile;
+        // warp-uniform decisions only: every tcgen05.ld/st below is .sync.aligned
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_s_full + 8 * t, j & 1, p.status, kWhereKv8Softmax))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s[128];
+        tmem_ld32(s_addr + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+        tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+        tmem_ld32(s_addr + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+        tmem_ld32(s_addr + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+        const float4* sc = scales + (j & 3) * 8;
+        tmem_ld_wait();
+        if (kbase + kTile > lim) {
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            if (kbase + e >= lim) s[e] = 0xff800000u;
+        }
+        float m_new = m;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          float a = __uint_as_float(s[16 * g]), d = __uint_as_float(s[16 * g + 1]);
+#pragma unroll
+          for (int e = 2; e < 16; e += 4) {
+            a = fmax3(a, __uint_as_float(s[16 * g + e]), __uint_as_float(s[16 * g + e + 1]));
+            if (e + 2 < 16) d = fmax3(d, __uint_as_float(s[16 * g + e + 2]), __uint_as_float(s[16 * g + e + 3]));
+          }
+          const float4 k = sc[g];
+          m_new = fmaxf(m_new, fmaf(fmaxf(a, d), fac * k.x, k.y));
+        }
+        const bool first = m == -INFINITY;
+        const bool need = !first && m_new > m + kFollow;
+        float factor = 1.f;
+        if (first) {
+          m = m_new;
+        } else if (need) {
+          factor = ex2_approx(m - m_new);
+          m = m_new;
+          l *= factor;
+        }
+        if (__any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+          for (int i = 0; i < HD / 32; ++i) {
+            uint32_t ov[32];
+            tmem_ld32(o_addr + 32 * i, ov);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * factor);
+            tmem_st32(o_addr + 32 * i, ov);
+          }
+          tmem_st_wait();
+        }
+        const float mu = m == -INFINITY ? 0.f : m - kTileBias;
+#pragma unroll
+        for (int g2 = 0; g2 < 4; ++g2) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const float4 k = sc[2 * g2 + g];
+            const float f = fac * k.x, off = k.y - mu;
+            float rs0 = 0.f, rs1 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float p0 = ex2_approx(fmaf(__uint_as_float(s[32 * g2 + 16 * g + 2 * e]), f, off));
+              const float p1 = ex2_approx(fmaf(__uint_as_float(s[32 * g2 + 16 * g + 2 * e + 1]), f, off));
+              rs0 += p0;
+              rs1 += p1;
+              pk[8 * g + e] = pack_f16x2(p0, p1);
+            }
+            l = fmaf(rs0 + rs1, k.z, l);
+          }
+          tmem_st16(s_addr + 16 * g2, pk);
+          if (g2 == 1) {  // P of keys 0-63 is in TMEM: PV over them may start
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_p_half + 8 * t);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p_full + 8 * t);
+      }
+    }
+    const float ref = m - kTileBias;  // o = sum 2^(x - ref) v8, l = sum 2^(x - ref) / vs
+    if (t == 0 || two) {
+      if (n_vis > 0) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar_o_done, 0, p.status, kWhereKv8Softmax));
+        tc_fence_after();
+      }
+      const bool store = valid && dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store);
+      const bool none = l == 0.f;  // the row saw nothing here
+      const int64_t pr = ((int64_t)split * plan.n_tail + (item - plan.n_full)) * 2 * kTile + t * kTile + lane_base + lane;
+      const float inv = splits > 1 ? 1.f : 1.f / l;
+      if (store && ok) {
+        if (splits > 1)
+          p.part_ml[pr] = make_float2(none ? -INFINITY : ref, l);
+        else if (p.lse)
+          p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = none ? -INFINITY : (ref + log2f(l)) * kLn2;
+      }
+      __nv_bfloat16* dst = p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD;
+      float* pdst = p.part_o + pr * HD;
+      if (ok) {
+#pragma unroll 1
+        for (int i = 0; i < HD / 32; ++i) {
+          uint32_t ov[32];
+          if (n_vis > 0) {
+            tmem_ld32(o_addr + 32 * i, ov);
+            tmem_ld_wait();
+          }
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : __uint_as_float(ov[e]) * inv;
+          if (store && splits > 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(pdst + 32 * i + 4 * e) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          } else if (store) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint4 x;
+              x.x = pack_bf16x2(v[8 * e], v[8 * e + 1]);
+              x.y = pack_bf16x2(v[8 * e + 2], v[8 * e + 3]);
+              x.z = pack_bf16x2(v[8 * e + 4], v[8 * e + 5]);
+              x.w = pack_bf16x2(v[8 * e + 6], v[8 * e + 7]);
+              *reinterpret_cast<uint4*>(dst + 32 * i + 8 * e) = x;
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem_base, 512);
+}
+
+// Joins the key splits of the tail items' rows, in split order; a thread has 8 columns.
+template <int HD>
+__global__ void __launch_bounds__(256) tile_join_kernel(const __grid_constant__ Cache c, const __grid_constant__ Query p,
+                                                        const __grid_constant__ TilePlan plan) {
+  pdl_trigger();
+  pdl_wait();
+  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t rows = (int64_t)plan.n_tail * 2 * kTile;
+  if (u >= rows * (HD / 8)) return;
+  const int64_t pr = u / (HD / 8);
+  const int col = (int)(u % (HD / 8)) * 8;
+  const int32_t heads = c.batch * c.n_kv, item = plan.n_full + (int32_t)(pr / (2 * kTile));
+  const int32_t bg = item % heads, b = bg / c.n_kv, kvh = bg % c.n_kv;
+  const int32_t pair = p.causal ? plan.pairs - 1 - item / heads : item / heads;
+  const int64_t r = (int64_t)pair * 2 * kTile + pr % (2 * kTile);
+  if (r >= p.n_rows) return;
+  float acc[8], lse;
+  join_row<HD>(p.part_o, p.part_ml, plan.splits, rows, pr, col, acc, lse);
+  const int64_t qi = r / p.group;
+  const int32_t h = kvh * p.group + (int32_t)(r % p.group);
+  if (!dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store)) return;
+  store_o8(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col, acc);
+  if (col == 0 && p.lse) p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = lse;
+}
+
+// ------------------------------------------------------------------ weighing
+constexpr int kWeighThreads = 640;  // warps 0-3: TMA, MMA; four warpgroups of rows
+constexpr int kWeighMaxCluster = 8;
+
+template <int HD>
+struct WeighCfg {
+  static constexpr int kTileBytes = kTile * HD * 2;
+  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 256 + 4 * 4 * 8 * 4 + kWeighMaxCluster * 16 * 4 + 1024;
+  static constexpr uint32_t kIdesc = idesc_bf16_f32(kTile, kTile, false, false);
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// q_tile: queries of a tile (kTile / group), its rows q_tile * group <= 128.
+template <int HD>
+__global__ void __launch_bounds__(kWeighThreads, 1)
+    tile_weigh_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ Cache c,
+                      const __grid_constant__ Query p, float decay, float* __restrict__ weight, int32_t q_tile) {
+  using C = WeighCfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sK = smem_u32(smem);
+  const uint32_t sQ = sK + 2 * C::kTileBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (2 + kSlots) * C::kTileBytes);
+  const uint32_t bar_q_full = smem_u32(bars);              // [kSlots]
+  const uint32_t bar_q_empty = bar_q_full + 8 * kSlots;    // [kSlots]
+  const uint32_t bar_s_full = bar_q_empty + 8 * kSlots;    // [4]
+  const uint32_t bar_s_empty = bar_s_full + 32;            // [4]
+  const uint32_t bar_done = bar_s_empty + 32;              // [1]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kSlots + 9);
+  float* sums = reinterpret_cast<float*>(smem + (2 + kSlots) * C::kTileBytes + 256);  // [4 warpgroups][4 warps][8 groups]
+  float* parts = sums + 4 * 4 * 8;                                                    // [cluster][16 groups]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank(), ranks = gridDim.z;
+  const int32_t bg = blockIdx.y, b = bg / c.n_kv, kvh = bg % c.n_kv;
+  const int32_t k0 = (int32_t)blockIdx.x * 2 * kTile;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(bar_q_full + 8 * s, 1);
+      mbar_init(bar_q_empty + 8 * s, 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(bar_s_full + 8 * s, 1);
+      mbar_init(bar_s_empty + 8 * s, 4);
+    }
+    mbar_init(bar_done, 1);
+    fence_barrier_init();
+  }
+  pdl_trigger();
+  pdl_wait();
+  const int32_t len = shown_rows(c, b, p.n_new, p.status, threadIdx.x == 0 && rank == 0);
+  if (k0 >= len) return;  // the whole cluster
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  const int32_t k_end = k0 + 2 * kTile < len ? k0 + 2 * kTile : len;
+  const bool two = k0 + kTile < k_end;
+  const int32_t tile_rows = q_tile * p.group;
+  // query tiles of this CTA: those that see a key of its range (causal: the last ones), shared by the cluster
+  const int32_t n_all = (int32_t)((p.n_q + q_tile - 1) / q_tile);
+  int32_t i_first = 0;
+  if (p.causal) {  // query i sees keys <= len - n_q + i
+    const int64_t q_first = (int64_t)k0 - (len - p.n_q);
+    if (q_first > 0) i_first = (int32_t)(q_first / q_tile);  // < n_all as k0 < len
+  }
+  const int32_t i0 = i_first + (int32_t)((int64_t)(n_all - i_first) * rank / ranks);
+  const int32_t i1 = i_first + (int32_t)((int64_t)(n_all - i_first) * (rank + 1) / ranks);
+  const int32_t n_i = i1 - i0;
+
+  if (n_i > 0 && warp >= 4) {
+    // the keys, widened to bf16 (exact), rows behind the end zero; the rows of a query tile that TMA never writes, zero
+    constexpr int kUnits = HD / 16, kStep = 512 / kUnits;
+    const int ct = (int)threadIdx.x - 128, u = ct % kUnits;
+    const uint8_t* src = c.k + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD + u * 16;
+#pragma unroll
+    for (int i = 0; i < 2 * kTile / kStep; ++i) {
+      const int row = ct / kUnits + i * kStep;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (k0 + row < k_end) w = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(k0 + row) * c.ld));
+      const uint32_t* x = reinterpret_cast<const uint32_t*>(&w);
+      uint32_t y[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = cvt_lo(x[e]), hi = cvt_hi(x[e]);
+        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+        y[2 * e] = pack_bf16x2(f0.x, f0.y);
+        y[2 * e + 1] = pack_bf16x2(f1.x, f1.y);
+      }
+      const uint32_t dst = sK + (row >> 7) * C::kTileBytes;
+      st_shared16(dst + sw_offset(row & 127, 2 * u), y[0], y[1], y[2], y[3]);
+      st_shared16(dst + sw_offset(row & 127, 2 * u + 1), y[4], y[5], y[6], y[7]);
+    }
+    const int pieces = (kTile - tile_rows) * (HD / 8);
+    for (int i = ct; i < kSlots * pieces; i += 512) {
+      const int q = i % pieces;
+      st_shared16(sQ + (i / pieces) * C::kTileBytes + sw_offset(tile_rows + q / (HD / 8), q % (HD / 8)), 0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  if (ranks > 1)
+    cluster_sync();  // the first CTA of the cluster has started before anything is written to it
+  else
+    __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+
+  if (warp == 0) {
+    if (lane == 0 && n_i > 0) {
+      tma_prefetch_desc(&tmap_q);
+      int armed = 0;
+      for (int i = 0; i < n_i; ++i) {
+        const int slot = i % kSlots;
+        if (!mbar_wait(bar_q_empty + 8 * slot, ((i / kSlots) & 1) ^ 1, p.status, kWhereKv8Widen)) break;
+        mbar_arrive_expect_tx(bar_q_full + 8 * slot, (uint32_t)tile_rows * HD * 2);
+        for (int bx = 0; bx < HD / 64; ++bx)
+          tma_load_4d(sQ + slot * C::kTileBytes + bx * kBoxBytes, &tmap_q, bar_q_full + 8 * slot, bx * 64,
+                      kvh * p.group, (i0 + i) * q_tile, b);
+        armed = i + 1;
+      }
+      // every copy lands before the CTA may exit
+      for (int i = armed > kSlots ? armed - kSlots : 0; i < armed; ++i) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(bar_q_full + 8 * (i % kSlots), (i / kSlots) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && n_i > 0) {
+      bool ok = true;
+      for (int i = 0; i < n_i && ok; ++i) {
+        const int slot = i % kSlots;
+        ok = mbar_wait(bar_q_full + 8 * slot, (i / kSlots) & 1, p.status, kWhereKv8Mma);
+        for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
+          const int buf = 2 * (i & 1) + t;
+          ok = mbar_wait(bar_s_empty + 8 * buf, ((i >> 1) & 1) ^ 1, p.status, kWhereKv8Mma);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t qa = sQ + slot * C::kTileBytes, ka = sK + t * C::kTileBytes;
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k) {
+            const uint32_t off = (k >> 2) * kBoxBytes + (k & 3) * 32;
+            umma_ss(tmem_base + 128u * buf, sw128_desc(qa + off, 16, 1024), sw128_desc(ka + off, 16, 1024), C::kIdesc,
+                    k > 0 ? 1u : 0u);
+          }
+          umma_commit(bar_s_full + 8 * buf);
+        }
+        if (ok) umma_commit(bar_q_empty + 8 * slot);
+      }
+      umma_commit(bar_done);
+      mbar_wait(bar_done, 0, p.status, kWhereKv8Drain);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int wg = (warp - 4) >> 2, t = wg & 1, phase = wg >> 1;
+    const int lane_base = (warp & 3) * 32, row = lane_base + lane;
+    const int32_t kbase = k0 + t * kTile;
+    float acc[8];
+    float f[8];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      acc[g] = 0.f;
+      const int32_t key = kbase + 16 * g;
+      f[g] = key < k_end ? p.scale_log2 * __ldg(c.k_scale + (int64_t)bg * c.n_blocks + key / c.block) : 0.f;
+    }
+    const int32_t qr = row / p.group, hr = row % p.group;  // query and head of this row in a tile
+    const float* lse_row = p.lse + ((int64_t)b * p.n_heads + kvh * p.group + hr) * p.n_q;
+    const uint32_t addr = tmem_base + ((uint32_t)lane_base << 16) + 128u * wg;
+    if (t == 0 || two) {
+#pragma unroll 1
+      for (int i = phase; i < n_i; i += 2) {
+        const int64_t qi = (int64_t)(i0 + i) * q_tile + qr;
+        // rows that are not there weigh 2^-inf; rows that saw nothing (lse = -inf) are hidden from every key
+        float ls = INFINITY;
+        int32_t lim = k_end;
+        if (row < tile_rows && qi < p.n_q) {
+          ls = __ldg(lse_row + qi) * kLog2e;
+          if (p.causal) {
+            const int64_t x = (int64_t)len - p.n_q + qi + 1;
+            lim = x < 0 ? 0 : (x < k_end ? (int32_t)x : k_end);
+          }
+          if (ls == -INFINITY) lim = 0;
+        }
+        const bool masked = kbase + kTile > lim;
+        const bool any = __any_sync(0xffffffffu, lim > kbase);
+        const bool ok =
+            __all_sync(0xffffffffu, mbar_wait(bar_s_full + 8 * wg, (i >> 1) & 1, p.status, kWhereKv8Softmax));
+        if (!ok) break;
+        tc_fence_after();
+        if (!any) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_s_empty + 8 * wg);
+          continue;
+        }
+        uint32_t s[2][32];
+        tmem_ld32(addr, s[0]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          tmem_ld_wait();
+          if (q < 3) {
+            tmem_ld32(addr + 32 * (q + 1), s[(q + 1) & 1]);
+          } else {  // S is in registers: the next product may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_s_empty + 8 * wg);
+          }
+          uint32_t(&x)[32] = s[q & 1];
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float pe = ex2_approx(fmaf(__uint_as_float(x[e]), f[2 * q + (e >> 4)], -ls));
+              acc[2 * q + (e >> 4)] += kbase + 32 * q + e < lim ? pe : 0.f;
+            }
+          } else {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                a0 += ex2_approx(fmaf(__uint_as_float(x[16 * g + e]), f[2 * q + g], -ls));
+                a1 += ex2_approx(fmaf(__uint_as_float(x[16 * g + e + 1]), f[2 * q + g], -ls));
+              }
+              acc[2 * q + g] += a0 + a1;
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) acc[g] += __shfl_xor_sync(0xffffffffu, acc[g], off);
+      if (lane == g) sums[(wg * 4 + (warp & 3)) * 8 + g] = acc[g];
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, 512);
+  // 16 group sums of this CTA, then of the cluster, each added in a fixed order
+  if (threadIdx.x < 16) {
+    const int t = threadIdx.x >> 3, g = threadIdx.x & 7;
+    float x = 0.f;
+#pragma unroll
+    for (int ph = 0; ph < 2; ++ph)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) x += sums[((2 * ph + t) * 4 + w) * 8 + g];
+    if (ranks > 1) {
+      const uint32_t at = mapa_shared(smem_u32(parts + rank * 16 + threadIdx.x), 0);
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+    } else {
+      parts[threadIdx.x] = x;
+    }
+  }
+  __syncwarp();
+  if (ranks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  const int n_groups = c.block / 16;  // groups of a block
+  if (rank == 0 && (int)threadIdx.x < 16 / n_groups) {
+    const int32_t key = k0 + (int32_t)threadIdx.x * c.block;
+    if (key < k_end) {
+      float x = 0.f;
+      for (uint32_t r = 0; r < ranks; ++r)
+        for (int g = 0; g < n_groups; ++g) x += parts[r * 16 + threadIdx.x * n_groups + g];
+      const int32_t blk = key / c.block;
+      if (dcheck(blk < c.n_blocks, p.status, kWhereKv8Store)) {
+        float* w = weight + (int64_t)bg * c.n_blocks + blk;
+        *w = fmaf(decay, *w, x);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+TilePlan make_plan(const Cache& c, const Query& p, int32_t max_len) {
+  TilePlan t{};
+  t.pairs = (int32_t)((p.n_rows + 2 * kTile - 1) / (2 * kTile));
+  const int64_t heads = (int64_t)c.batch * c.n_kv, items = heads * t.pairs, sms = num_sms();
+  const int64_t n_kt = ((int64_t)max_len + kTile - 1) / kTile;
+  t.splits = 1;
+  t.n_full = (int32_t)items;
+  // Items of a last wave that does not fill the SMs are split over the keys so
+  // that it does (items of a single query tile take about half as long).
+  const int64_t tail = items % sms;
+  const bool single = (p.n_rows - 1) % (2 * kTile) < kTile;
+  const double load = (double)tail - (single && !p.causal ? 0.45 * (double)(tail < heads ? tail : heads) : 0.0);
+  if (tail > 0) {
+    int64_t s = (int64_t)((double)sms / load + 0.25);
+    if (s > n_kt / 2) s = n_kt / 2;
+    if (s > 1) {
+      t.splits = (int32_t)s;
+      t.n_tail = (int32_t)tail;
+      t.n_full = (int32_t)(items - tail);
+    }
+  }
+  return t;
+}
+
+size_t plan_o_bytes(const TilePlan& t, int hd) {
+  return ((size_t)t.splits * t.n_tail * 2 * kTile * hd * 4 + 255) & ~size_t(255);
+}
+
+// Sets a kernel's shared-memory limit once per device; `regs`, if not 0, is
+// the sum that its register hand-over needs of the launch.
+template <typename K>
+cosmot_status prepare(K kern, int smem, int64_t regs, int threads, uint64_t& done) {
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return COSMOT_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(mu);
+  if (dev < 64 && (done & (1ull << dev))) return COSMOT_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return COSMOT_ERR_CUDA;
+  if (regs) {
+    // a build whose register count cannot fund the hand-over is not launched
+    cudaFuncAttributes fa{};
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || regs > (int64_t)threads * fa.numRegs) return COSMOT_ERR_CUDA;
+  }
+  if (dev < 64) done |= 1ull << dev;
+  return COSMOT_OK;
+}
+
+template <int HD>
+cosmot_status launch_attention(const Cache& c, const Query& p, const TilePlan& t, cudaStream_t s) {
+  static uint64_t done = 0;
+  cosmot_status st = prepare(tile_attention_kernel<HD>, AttnCfg<HD>::kSmem,
+                             128 * (kRegsMma + kRegsConv) + 256 * kRegsSoftmax, kAttnThreads, done);
+  if (st != COSMOT_OK) return st;
+  const int64_t grid = t.n_full + (int64_t)t.n_tail * t.splits;
+  st = launch_status(launch_pdl(tile_attention_kernel<HD>, dim3((unsigned)grid), dim3(kAttnThreads), AttnCfg<HD>::kSmem, s,
+                                nullptr, c, p, t));
+  if (st != COSMOT_OK || t.n_tail == 0) return st;
+  const int64_t units = (int64_t)t.n_tail * 2 * kTile * (HD / 8);
+  return launch_status(launch_pdl(tile_join_kernel<HD>, dim3((unsigned)((units + 255) / 256)), dim3(256), 0, s, nullptr, c,
+                                  p, t));
+}
+
+template <int HD>
+cosmot_status launch_weigh(const Cache& c, const Query& p, float decay, float* weight, int32_t max_len, cudaStream_t s) {
+  static uint64_t done = 0;
+  cosmot_status st = prepare(tile_weigh_kernel<HD>, WeighCfg<HD>::kSmem, 0, kWeighThreads, done);
+  if (st != COSMOT_OK) return st;
+  const int32_t q_tile = kTile / p.group;
+  CUtensorMap map;
+  st = make_tmap_bf16_4d(&map, p.q, (uint64_t)HD, (uint64_t)p.n_heads, (uint64_t)p.n_q, (uint64_t)c.batch, (uint64_t)p.ld_q,
+                         (uint64_t)(c.batch > 1 ? p.q_bstride : p.n_q), 64, (uint32_t)p.group, (uint32_t)q_tile);
+  if (st != COSMOT_OK) return st;
+  const int64_t heads = (int64_t)c.batch * c.n_kv, n_all = (p.n_q + q_tile - 1) / q_tile;
+  const int64_t live = heads * (((int64_t)max_len + 2 * kTile - 1) / (2 * kTile));
+  // a key range's queries are shared by a cluster where there are fewer key ranges than SMs
+  unsigned ranks = 1;
+  while (ranks < (unsigned)kWeighMaxCluster && live * ranks * 2 <= num_sms() && n_all >= 4 * ranks) ranks *= 2;
+  cudaLaunchAttribute cl{};
+  cl.id = cudaLaunchAttributeClusterDimension;
+  cl.val.clusterDim.x = 1;
+  cl.val.clusterDim.y = 1;
+  cl.val.clusterDim.z = ranks;
+  const dim3 grid((unsigned)((c.capacity + 2 * kTile - 1) / (2 * kTile)), (unsigned)heads, ranks);
+  return launch_status(launch_pdl(tile_weigh_kernel<HD>, grid, dim3(kWeighThreads), WeighCfg<HD>::kSmem, s, &cl, map, c, p,
+                                  decay, weight, q_tile));
+}
+
+}  // namespace
+
+size_t tile_workspace(const Cache& c, const Query& p, int32_t max_len) {
+  const TilePlan t = make_plan(c, p, max_len);
+  return t.n_tail == 0 ? 0 : plan_o_bytes(t, c.hd) + (size_t)t.splits * t.n_tail * 2 * kTile * sizeof(float2);
+}
+
+cosmot_status tile_attention(const Cache& c, const Query& p0, int32_t max_len, void* workspace, cudaStream_t s) {
+  Query p = p0;
+  const TilePlan t = make_plan(c, p, max_len);
+  if ((int64_t)c.batch * c.n_kv * t.pairs > INT32_MAX / 64) return COSMOT_ERR_UNSUPPORTED;
+  if (t.n_tail) {
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan_o_bytes(t, c.hd));
+  }
+  return c.hd == 128 ? launch_attention<128>(c, p, t, s) : launch_attention<64>(c, p, t, s);
+}
+
+cosmot_status tile_weigh(const Cache& c, const Query& p, float decay, float* weight, int32_t max_len, cudaStream_t s) {
+  return c.hd == 128 ? launch_weigh<128>(c, p, decay, weight, max_len, s)
+                     : launch_weigh<64>(c, p, decay, weight, max_len, s);
+}
+
+}  // namespace kv8
+}  // namespace cosmot

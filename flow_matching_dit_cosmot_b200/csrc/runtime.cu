@@ -76,6 +76,22 @@ cosmot_status make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t row
   return r == CUDA_SUCCESS ? COSMOT_OK : COSMOT_ERR_INVALID_ARG;
 }
 
+cosmot_status make_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3,
+                                uint64_t ld, uint64_t ld3, uint32_t box0, uint32_t box1, uint32_t box2) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return COSMOT_ERR_CUDA;
+  if (!aligned16(base) || (d0 * 2) % 16 != 0 || (ld * 2) % 16 != 0 || d0 == 0 || d1 == 0 || d2 == 0 || d3 == 0)
+    return COSMOT_ERR_INVALID_ARG;
+  cuuint64_t dims[4] = {d0, d1, d2, d3};
+  cuuint64_t strides[3] = {d0 * 2, ld * 2, ld3 * ld * 2};
+  cuuint32_t box[4] = {box0, box1, box2, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? COSMOT_OK : COSMOT_ERR_INVALID_ARG;
+}
+
 // Test-only: warp 0 is a producer that never arrives on the barrier; thread 32
 // waits for it with the library's bounded wait, which gives up after
 // kWaitLimitNs and latches COSMOT_ERR_TIMEOUT at kWhereSelftest.
