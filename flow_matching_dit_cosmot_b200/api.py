@@ -7,6 +7,7 @@ and translate tensors into the pointers and structs the C entry points take.
 
 from __future__ import annotations
 
+import ctypes
 from dataclasses import dataclass
 from typing import Optional
 
@@ -244,6 +245,18 @@ def _rows_layout(t: torch.Tensor, name: str, batch: int, heads: Optional[int], h
     """(ld, rows between sequences) of a [batch, n, heads, head_dim] tensor whose
     rows hold their heads side by side; a view of a wider row (the columns of a
     QKV projection) fits."""
+    if t.dtype is dtype and t.dim() == 4:  # the usual tensor, without the detours below
+        b, rows, h, hd = t.shape
+        s0, s1, s2, s3 = t.stride()
+        if b == batch and hd == head_dim and (h == heads or heads is None) and (rows == n or n is None) and s3 == 1 and \
+                h > 0 and (s2 == hd or h == 1):
+            if rows == 1 and (s0 >= h * hd or batch == 1):
+                return (s0, 1) if batch > 1 else (h * hd, 1)
+            if rows > 1 and s1 >= h * hd:
+                if batch == 1:
+                    return s1, rows
+                if s0 % s1 == 0 and s0 >= rows * s1:
+                    return s1, s0 // s1
     if t.dim() != 4 or t.shape[0] != batch or t.shape[3] != head_dim or (heads is not None and t.shape[2] != heads) or \
             (n is not None and t.shape[1] != n):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{batch}, {'n' if n is None else n}, "
@@ -312,6 +325,9 @@ class KVCache8:
         self.device = k.device
         self.desc = L.Kv8Cache(ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), ptr(lens), layout[0], layout[1], batch,
                                capacity, n_kv, hd, block, 0)
+        self._ref = ctypes.byref(self.desc)
+        self._plans = {}
+        self._evict_bytes = None
 
     @classmethod
     def empty(cls, batch: int, capacity: int, n_kv_heads: int, head_dim: int, block: int = 64, device="cuda"):
@@ -326,42 +342,68 @@ class KVCache8:
 
     @staticmethod
     def _check(name, t, dtype, shape):
-        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} (got {t.dtype}, "
                              f"{tuple(t.shape)}, {'contiguous' if t.is_contiguous() else 'strided'})")
 
-    def _here(self, *named):
-        for name, t in named:
-            if t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
+    def _here(self, name: str, t: torch.Tensor):
+        if t.get_device() != self.device.index:
+            raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
 
-    def _stream(self, stream, *made):
-        """The stream's handle; tensors made here are kept until it is done with them."""
-        if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
+    def _stream(self, stream, *made) -> int:
+        """The stream's handle.  Tensors made here come from the current stream's memory: another
+        stream waits for what that stream still does with it, and they are kept until it is done."""
+        if stream is None:  # torch.cuda.current_stream(device).cuda_stream, without the object
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
         if stream.device != self.device:
             raise ValueError(f"the stream is on {stream.device}, the cache on {self.device}")
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
+        made = [t for t in made if t is not None]
+        if made:
+            current = torch.cuda.current_stream(self.device)
+            if current != stream:
+                stream.wait_stream(current)
+                for t in made:
+                    t.record_stream(stream)
         return stream.cuda_stream
+
+    def _call(self, name: str, *args):
+        """One of the library's entries, on the cache's device."""
+        fn = getattr(L.lib(), name)
+        if torch.cuda.current_device() == self.device.index:
+            code = fn(self._ref, *args)
+        else:
+            with torch.cuda.device(self.device):
+                code = fn(self._ref, *args)
+        if code != L.COSMOT_OK:
+            raise L.CosmotError(name, code)
 
     def _workspace(self, need: int, workspace: Optional[torch.Tensor]):
         """(tensor, made here): the caller's workspace, or one for this call."""
         if workspace is not None:
-            self._here(("workspace", workspace))
+            self._here("workspace", workspace)
             if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
                 raise ValueError(f"workspace: expected at least {need} contiguous uint8 elements")
             return workspace, None
-        made = torch.empty((need,), dtype=torch.uint8, device=self.device) if need else None
+        made = self.k_scale.new_empty((need,), dtype=torch.uint8) if need else None
         return made, made
 
-    def _query(self, q: torch.Tensor, n_new: int, causal: bool, max_len: int, softmax_scale: float):
+    def _query(self, q: torch.Tensor, n_new: int, causal: bool, max_len: int, softmax_scale: float, o_between: int = 0):
+        """(descriptor, attention's workspace bytes, elements between q's rows).  The
+        first two depend on sizes alone and are kept for calls of the same sizes."""
         ld, between = _rows_layout(q, "q", self.batch, None, self.head_dim, torch.bfloat16)
-        self._here(("q", q))
-        desc = L.Kv8Query(q.shape[1], between, q.shape[1], q.shape[2], n_new,
-                          L.COSMOT_KV8_CAUSAL if causal else L.COSMOT_KV8_FULL, max_len, softmax_scale, 0)
-        return desc, ld
+        self._here("q", q)
+        n, heads = q.shape[1], q.shape[2]
+        key = (n, heads, between, o_between, n_new, causal, max_len, softmax_scale)
+        plan = self._plans.get(key)
+        if plan is None:
+            desc = L.Kv8Query(n, between, o_between or n, heads, n_new, L.COSMOT_KV8_CAUSAL if causal else L.COSMOT_KV8_FULL,
+                              max_len, softmax_scale, 0)
+            need = ctypes.c_size_t(0)
+            self._call("cosmot_kv8_attention_workspace", ctypes.byref(desc), ctypes.byref(need))
+            if len(self._plans) >= 64:
+                self._plans = {}
+            plan = self._plans[key] = (ctypes.byref(desc), need.value)
+        return plan[0], plan[1], ld
 
     def advance(self, n: int):
         """The last n stored rows become rows held (on the current stream)."""
@@ -370,14 +412,14 @@ class KVCache8:
     def store(self, k: torch.Tensor, v: torch.Tensor, stream=None):
         """Rows [batch, n, n_kv_heads, head_dim] (bf16, views of a QKV projection
         fit) behind the ones held; `advance` makes them held."""
-        layout = _rows_layout(k, "k", self.batch, self.n_kv_heads, self.head_dim, torch.bfloat16)
-        if _rows_layout(v, "v", self.batch, self.n_kv_heads, self.head_dim, torch.bfloat16, k.shape[1]) != layout:
+        n = k.shape[1] if k.dim() == 4 else None
+        ld, between = _rows_layout(k, "k", self.batch, self.n_kv_heads, self.head_dim, torch.bfloat16)
+        if _rows_layout(v, "v", self.batch, self.n_kv_heads, self.head_dim, torch.bfloat16, n) != (ld, between):
             raise ValueError("k and v must have the same strides")
-        self._here(("k", k), ("v", v))
-        if k.shape[1] == 0:
-            return
-        with torch.cuda.device(self.device):
-            L.cosmot_kv8_store(self.desc, ptr(k), ptr(v), layout[0], layout[1], k.shape[1], self._stream(stream))
+        self._here("k", k)
+        self._here("v", v)
+        if n:
+            self._call("cosmot_kv8_store", k.data_ptr(), v.data_ptr(), ld, between, n, self._stream(stream))
 
     def attend(self, q: torch.Tensor, n_new: int = 0, causal: bool = False, out: Optional[torch.Tensor] = None,
                lse: Optional[torch.Tensor] = None, max_len: int = 0, softmax_scale: float = 0.0,
@@ -387,25 +429,29 @@ class KVCache8:
         query i is row len - n + i and sees the rows up to itself; otherwise every
         row.  max_len: the most rows any sequence shows, if known (it sizes the
         split of the work only)."""
-        desc, ld = self._query(q, n_new, causal, max_len, softmax_scale)
+        if q.dim() != 4:
+            raise ValueError(f"q has shape {tuple(q.shape)}, expected [batch, n, heads, head_dim]")
+        batch, n, heads, hd = q.shape
         made = []
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
+            out = q.new_empty((batch, n, heads, hd))
             made.append(out)
+            ld_o, o_between = heads * hd, n
+        else:
+            ld_o, o_between = _rows_layout(out, "out", self.batch, heads, self.head_dim, torch.bfloat16, n)
+            self._here("out", out)
         if lse is None:
-            lse = torch.empty((self.batch, q.shape[2], q.shape[1]), device=self.device)
+            lse = self.k_scale.new_empty((batch, heads, n))
             made.append(lse)
-        ld_o, desc.o_batch_stride = _rows_layout(out, "out", self.batch, q.shape[2], self.head_dim, torch.bfloat16,
-                                                 q.shape[1])
-        self._check("lse", lse, torch.float32, (self.batch, q.shape[2], q.shape[1]))
-        self._here(("out", out), ("lse", lse))
-        if q.shape[1] == 0:
+        else:
+            self._check("lse", lse, torch.float32, (batch, heads, n))
+            self._here("lse", lse)
+        desc, need, ld = self._query(q, n_new, causal, max_len, softmax_scale, o_between)
+        if n == 0:
             return out, lse
-        with torch.cuda.device(self.device):
-            need = L.cosmot_kv8_attention_workspace(self.desc, desc)
-            ws, fresh = self._workspace(need, workspace)
-            L.cosmot_kv8_attention(self.desc, desc, ptr(q), ld, ptr(out), ld_o, ptr(lse), ptr(ws),
-                                   0 if ws is None else ws.numel(), self._stream(stream, *made, fresh))
+        ws, fresh = self._workspace(need, workspace)
+        self._call("cosmot_kv8_attention", desc, q.data_ptr(), ld, out.data_ptr(), ld_o, lse.data_ptr(), ptr(ws),
+                   0 if ws is None else ws.numel(), self._stream(stream, *made, fresh))
         return out, lse
 
     def weigh(self, q: torch.Tensor, lse: torch.Tensor, weight: torch.Tensor, decay: float = 1.0, n_new: int = 0,
@@ -413,15 +459,14 @@ class KVCache8:
         """weight [batch, n_kv_heads, blocks] = decay * weight + the attention
         weight of q's rows for each block; lse as `attend` gave it for the same
         query.  Returns weight."""
-        desc, ld = self._query(q, n_new, causal, max_len, softmax_scale)
-        desc.o_batch_stride = desc.n_q
+        desc, _, ld = self._query(q, n_new, causal, max_len, softmax_scale)
         self._check("lse", lse, torch.float32, (self.batch, q.shape[2], q.shape[1]))
         self._check("weight", weight, torch.float32, (self.batch, self.n_kv_heads, self.n_blocks))
-        self._here(("lse", lse), ("weight", weight))
+        self._here("lse", lse)
+        self._here("weight", weight)
         if q.shape[1] == 0:
             raise ValueError("weigh needs at least one query")
-        with torch.cuda.device(self.device):
-            L.cosmot_kv8_weigh(self.desc, desc, ptr(q), ld, ptr(lse), decay, ptr(weight), self._stream(stream))
+        self._call("cosmot_kv8_weigh", desc, q.data_ptr(), ld, lse.data_ptr(), decay, weight.data_ptr(), self._stream(stream))
         return weight
 
     def evict(self, weight: torch.Tensor, keep_blocks: int, first_rows: int = 0, last_rows: int = 0,
@@ -432,11 +477,12 @@ class KVCache8:
         scales move up in place; (weight, lens) follow in place too, or, with
         in_place=False, are returned as new tensors."""
         self._check("weight", weight, torch.float32, (self.batch, self.n_kv_heads, self.n_blocks))
-        self._here(("weight", weight))
+        self._here("weight", weight)
         w_out, lens = (weight, self.lens) if in_place else (torch.empty_like(weight), torch.empty_like(self.lens))
-        with torch.cuda.device(self.device):
-            ws, fresh = self._workspace(L.cosmot_kv8_evict_workspace(self.desc), workspace)
-            made = (fresh,) if in_place else (fresh, w_out, lens)
-            L.cosmot_kv8_evict(self.desc, ptr(weight), keep_blocks, first_rows, last_rows, ptr(w_out), ptr(lens),
-                               ptr(ws), ws.numel(), self._stream(stream, *made))
+        if self._evict_bytes is None:
+            self._evict_bytes = L.cosmot_kv8_evict_workspace(self.desc)
+        ws, fresh = self._workspace(self._evict_bytes, workspace)
+        made = (fresh,) if in_place else (fresh, w_out, lens)
+        self._call("cosmot_kv8_evict", weight.data_ptr(), keep_blocks, first_rows, last_rows, w_out.data_ptr(),
+                   lens.data_ptr(), ws.data_ptr(), ws.numel(), self._stream(stream, *made))
         return w_out, lens
