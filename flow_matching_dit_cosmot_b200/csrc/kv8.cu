@@ -422,7 +422,7 @@ extern "C" cosmot_status cosmot_kv8_attention_workspace(const cosmot_kv8_cache* 
     *bytes = kv8::tile_workspace(c, p, kv8::bound_len(cache, query));
     return COSMOT_OK;
   }
-  p.splits = kv8::rows_splits(c, p, kv8::bound_len(cache, query));
+  kv8::rows_plan(c, p, kv8::bound_len(cache, query));
   *bytes = kv8::part_bytes(c, p);
   return COSMOT_OK;
 }
@@ -439,7 +439,7 @@ extern "C" cosmot_status cosmot_kv8_attention(const cosmot_kv8_cache* cache, con
   if (!o || !aligned16(o) || ld_o % 8 || ld_o < (int64_t)p.n_heads * c.hd) return COSMOT_ERR_INVALID_ARG;
   const int32_t max_len = kv8::bound_len(cache, query);
   const bool tiles = kv8::use_tiles(p);
-  if (!tiles) p.splits = kv8::rows_splits(c, p, max_len);
+  if (!tiles) kv8::rows_plan(c, p, max_len);
   const size_t need = tiles ? kv8::tile_workspace(c, p, max_len) : kv8::part_bytes(c, p);
   if (need > 0) {
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return COSMOT_ERR_INVALID_ARG;

@@ -47,7 +47,7 @@ struct Query {
   int32_t causal;
   float scale_log2;  // softmax scale * log2(e)
   // split of the keys (workspace): O'' [split][batch][n_kv][n_rows][hd] and (m, l)
-  int32_t splits;
+  int32_t splits, chunk;  // chunk: keys of a split (register-tile kernels)
   float* part_o;
   float2* part_ml;
   int* status;
@@ -162,8 +162,8 @@ cosmot_status make_query(const cosmot_kv8_cache* c, const cosmot_kv8_query* d, Q
 // Register-tile kernels (kv8_rows.cu): few packed rows.
 cosmot_status rows_attention(const Cache& c, const Query& p, cudaStream_t s);
 cosmot_status rows_weigh(const Cache& c, const Query& p, float decay, float* weight, cudaStream_t s);
-// Key split of a register-tile attention call.
-int32_t rows_splits(const Cache& c, const Query& p, int32_t max_len);
+// Sets the key split of a register-tile attention call.
+void rows_plan(const Cache& c, Query& p, int32_t max_len);
 // tcgen05 kernels (kv8_tile.cu): many packed rows.  max_len: what the host
 // takes the longest sequence to show; it sizes the split of the work only.
 size_t tile_workspace(const Cache& c, const Query& p, int32_t max_len);

@@ -1,34 +1,76 @@
 // Attention and weighing over the 8-bit cache for few query rows (single
 // tokens), bound by the cache's bytes.
 //
-// A warp takes 16 keys at a time, straight from global memory into registers:
-// the fragment layouts of mma.m16n8k16 leave the order of the contracted
-// dimension and of the output columns free, so each lane loads 16 contiguous
-// bytes of a row and those bytes are its operands.
-//   S = Q K^T    lane (g, j) (g = lane / 4, j = lane % 4) loads dims 16j..16j+15
-//                of each 64-dim half of key g of an 8-key tile; chunk c of 4
-//                bytes is k-step c, slots (2j, 2j+1, 2j+8, 2j+9) = dims
-//                16j + 4c + (0, 1, 2, 3); Q is laid out the same way once.
-//   O += P V     the accumulator of S is the A operand of PV; lane (g, j) loads
-//                piece g (hd/8 bytes) of the rows of its four keys 2j, 2j+1,
-//                8 + 2j, 8 + 2j + 1; column tile i is byte i of every piece.
+// A warp takes 16 keys at a time.  Keys are the M dimension of mma.m16n8k16 and
+// eight packed query rows its N dimension, so that a row tile costs no more
+// products than it has to:
+//   S^T = K Q^T    lane (g, j) (g = lane / 4, j = lane % 4) holds bytes 16j ..
+//                  16j+15 of each 64-dim half of keys g and g + 8; chunk c of 4
+//                  bytes is k-step c, slots (2j, 2j+1, 2j+8, 2j+9) = dims
+//                  16j + 4c + (0, 1, 2, 3); Q is laid out the same way once.
+//   O^T += V^T P^T P^T (f16) is S^T's accumulator, transposed in registers
+//                  (movmatrix); lane (g, j) holds piece g (hd/8 bytes) of the
+//                  rows of its four keys 2j, 2j+1, 8 + 2j, 8 + 2j + 1; row tile
+//                  i is bytes 2i and 2i + 1 of every piece.
+// The contracted dimension's order and the output rows' order are free, so
+// every lane needs just the bytes that it loads itself: they go through a ring
+// of cp.async stages in shared memory that no other lane reads, with no
+// barrier, and leave the registers to the products.
 // Q (bf16) becomes f16 by a power of two per row that puts its largest
 // magnitude in [2^13, 2^14): exact down to 2^-31 of it.  P (f16) is kept times
-// 2^15: full precision for weights down to 2^-29 of the largest.
+// 2^8, and the running maximum follows only when it grows by more than 2^7:
+// full precision for weights down to 2^-22 of the largest.
 #include "kv8.cuh"
+
+#include <mutex>
 
 namespace cosmot {
 namespace kv8 {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr float kPBias = 15.f;
+constexpr int kRing = 4;       // stages of 16 keys in flight
+constexpr int kCtasPerSm = 3;  // shared memory and registers allow three
+constexpr float kPBias = 8.f, kFollow = 7.f;
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8x8 matrix of 16-bit elements held two a lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool live) {
+  const int n = live ? BYTES : 0;  // nothing is read for n = 0: the destination becomes zeros
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 ld_shared8(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
 }
 
 // One row's 16-dim pieces for this lane (its j), scaled into f16; returns the
@@ -47,13 +89,15 @@ __device__ __forceinline__ float load_q_row(const __nv_bfloat16* row, bool valid
       *reinterpret_cast<uint4*>(&w[h][0]) = __ldg(p);
       *reinterpret_cast<uint4*>(&w[h][4]) = __ldg(p + 1);
     }
+  }
+#pragma unroll
+  for (int h = 0; h < HD / 64; ++h)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float2 v = unpack_bf16x2(w[h][i]);
       amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
       finite = finite && fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY;
     }
-  }
 #pragma unroll
   for (int off = 1; off < 4; off <<= 1) {
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
@@ -73,355 +117,504 @@ __device__ __forceinline__ float load_q_row(const __nv_bfloat16* row, bool valid
   return finite ? exp2_int(e) : __int_as_float(0x7fc00000);
 }
 
-template <int HD>
-struct KFrag {
-  uint4 w[2][HD / 64];  // [8-key tile][64-dim half]
-};
-
-template <int HD>
-__device__ __forceinline__ void load_k(KFrag<HD>& f, const uint8_t* base, int64_t ld, int32_t key0, int32_t kend, int g,
-                                       int j) {
+// NT tiles of eight packed rows from r0: B fragments (this lane's row g), and
+// the score factors of the rows of its accumulator columns 2j and 2j + 1.
+template <int HD, int NT>
+__device__ __forceinline__ void load_q_tile(const Cache& c, const Query& p, int32_t b, int32_t kvh, int64_t r0, int g,
+                                            int j, uint32_t (&q)[NT][HD / 16][2], float (&fac)[NT][2]) {
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int h = 0; h < HD / 64; ++h) {
-      f.w[t][h] = make_uint4(0, 0, 0, 0);
-      if (key0 + 8 * t + g < kend)
-        f.w[t][h] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)(key0 + 8 * t + g) * ld + 64 * h + 16 * j));
-    }
+  for (int n = 0; n < NT; ++n) {
+    const int64_t r = r0 + 8 * n + g;
+    const bool valid = r < p.n_rows;
+    const int64_t qi = valid ? r / p.group : 0;
+    const int32_t h = kvh * p.group + (int32_t)(valid ? r % p.group : 0);
+    const float f = p.scale_log2 * load_q_row<HD>(p.q + (b * p.q_bstride + qi) * p.ld_q + (int64_t)h * HD, valid, j, q[n]);
+    fac[n][0] = __shfl_sync(0xffffffffu, f, 8 * j);
+    fac[n][1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
+  }
 }
 
-// S of one 8-key tile for MT tiles of 16 rows.
-template <int HD, int MT>
-__device__ __forceinline__ void scores(float (&s)[MT][4], const KFrag<HD>& f, int t, const uint32_t (&q)[MT][HD / 16][4]) {
+// S^T of 16 keys: ka, kb the 16-byte pieces of keys g and g + 8.
+template <int HD, int NT>
+__device__ __forceinline__ void scores(float (&s)[NT][4], const uint4 (&ka)[HD / 64], const uint4 (&kb)[HD / 64],
+                                       const uint32_t (&q)[NT][HD / 16][2]) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m) s[m][0] = s[m][1] = s[m][2] = s[m][3] = 0.f;
+  for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
   for (int h = 0; h < HD / 64; ++h) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&f.w[t][h]);
+    const uint32_t* a = reinterpret_cast<const uint32_t*>(&ka[h]);
+    const uint32_t* d = reinterpret_cast<const uint32_t*>(&kb[h]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t b0 = cvt_lo(w[c]), b1 = cvt_hi(w[c]);
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t a0 = cvt_lo(a[k]), a1 = cvt_lo(d[k]), a2 = cvt_hi(a[k]), a3 = cvt_hi(d[k]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) mma_f16(s[m], q[m][4 * h + c], b0, b1);
+      for (int n = 0; n < NT; ++n) mma_f16(s[n], a0, a1, a2, a3, q[n][4 * h + k][0], q[n][4 * h + k][1]);
     }
   }
 }
 
-template <int HD, int MT>
-__device__ __forceinline__ void load_q_tile(const Cache& c, const Query& p, int32_t b, int32_t kvh, int64_t r0, int g,
-                                            int j, uint32_t (&q)[MT][HD / 16][4], float (&fac)[MT][2]) {
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t r = r0 + 16 * m + 8 * i + g;
-      const bool valid = r < p.n_rows;
-      const int64_t qi = valid ? r / p.group : 0;
-      const int32_t h = kvh * p.group + (int32_t)(valid ? r % p.group : 0);
-      uint32_t f[HD / 16][2];
-      fac[m][i] = p.scale_log2 * load_q_row<HD>(p.q + (b * p.q_bstride + qi) * p.ld_q + (int64_t)h * HD, valid, j, f);
-#pragma unroll
-      for (int k = 0; k < HD / 16; ++k) {
-        q[m][k][i] = f[k][0];
-        q[m][k][2 + i] = f[k][1];
-      }
-    }
-}
-
 // ------------------------------------------------------------------ attention
-template <int HD, int MT>
-__global__ void __launch_bounds__(32 * kWarps) rows_attention_kernel(const Cache c, const Query p) {
+template <int HD>
+struct Ring {
+  static constexpr int kPieceK = 512;               // 16 bytes a lane
+  static constexpr int kPieceV = HD == 128 ? 512 : 256;
+  static constexpr int kOffV = 2 * (HD / 64) * kPieceK;
+  static constexpr int kOffS = kOffV + 4 * kPieceV;  // ks, vs: 4 bytes a lane each
+  static constexpr int kStage = kOffS + 256;
+  static constexpr int kRowPitch = HD + 4;           // floats between rows of the warps' parts
+  static constexpr int smem(int nt) {
+    const int ring = kWarps * kRing * kStage, parts = kWarps * 8 * nt * (kRowPitch * 4 + 8);
+    return ring > parts ? ring : parts;
+  }
+};
+
+// One CTA per (key range, 8 NT packed rows, sequence and key head); its warps
+// take 16 keys in turn.
+template <int HD, int NT>
+__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) rows_attention_kernel(const __grid_constant__ Cache c,
+                                                                                 const __grid_constant__ Query p) {
   pdl_trigger();
   pdl_wait();
-  constexpr int NT = HD / 8;  // column tiles of O = bytes of a V piece
-  extern __shared__ float sm[];
-  float* sm_o = sm;                                  // [kWarps][16 MT][HD]
-  float2* sm_ml = reinterpret_cast<float2*>(sm + kWarps * 16 * MT * HD);  // [kWarps][16 MT]
+  using R = Ring<HD>;
+  extern __shared__ __align__(16) uint8_t sm_raw[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
   const int32_t split = blockIdx.x;
   const int32_t b = blockIdx.z / c.n_kv, kvh = blockIdx.z % c.n_kv;
-  const int64_t r0 = (int64_t)blockIdx.y * 16 * MT;
+  const int64_t r0 = (int64_t)blockIdx.y * 8 * NT;
   const int32_t len = shown_rows(c, b, p.n_new, p.status, threadIdx.x == 0);
-  const int64_t r_last = (r0 + 16 * MT < p.n_rows ? r0 + 16 * MT : p.n_rows) - 1;
-  const int32_t kend = row_limit(p, r_last, len);
-  const int32_t n_grp = (kend + 15) >> 4;
-  const int32_t g0 = (int32_t)((int64_t)split * n_grp / p.splits);
-  const int32_t g1 = (int32_t)((int64_t)(split + 1) * n_grp / p.splits);
-
-  uint32_t q[MT][HD / 16][4];
-  float fac[MT][2];
-  load_q_tile<HD, MT>(c, p, b, kvh, r0, g, j, q, fac);
-  int32_t lim[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) lim[m][i] = row_limit(p, r0 + 16 * m + 8 * i + g, len);
+  const int64_t r_end = r0 + 8 * NT < p.n_rows ? r0 + 8 * NT : p.n_rows;
+  const int32_t shown = row_limit(p, r_end - 1, len);  // the tile's last row sees the most
+  // this CTA's keys; the last range takes what is left of a sequence longer than the host said
+  const int32_t k0 = (int32_t)min((int64_t)shown, (int64_t)split * p.chunk);
+  const int32_t kend = split == p.splits - 1 ? shown : (int32_t)min((int64_t)shown, (int64_t)(split + 1) * p.chunk);
+  if (p.splits > 1 && k0 >= kend) {  // nothing here: the join leaves this range out
+    if (r0 + threadIdx.x < r_end && threadIdx.x < 8 * NT)
+      p.part_ml[((int64_t)split * c.batch * c.n_kv + blockIdx.z) * p.n_rows + r0 + threadIdx.x] = make_float2(-INFINITY, 0.f);
+    return;
+  }
 
   const uint8_t* kb = c.k + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD;
   const uint8_t* vb = c.v + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD;
   const float* ksp = c.k_scale + (int64_t)blockIdx.z * c.n_blocks;
   const float* vsp = c.v_scale + (int64_t)blockIdx.z * c.n_blocks;
+  const int block_shift = 31 - __clz(c.block);
+  const uint32_t ring = smem_u32(sm_raw) + warp * kRing * R::kStage;
 
-  float o[MT][NT][4];
-  float mx[MT][2], l[MT][2];
+  auto fetch = [&](int32_t key0, int slot) {
+    if (key0 < kend) {
+      const uint32_t st = ring + slot * R::kStage + lane * 16;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+      for (int t = 0; t < 2; ++t) {
+        const int32_t key = key0 + 8 * t + g;
+        const bool live = key < kend;
+        const uint8_t* src = kb + (int64_t)(live ? key : key0) * c.ld + 16 * j;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[m][i][0] = o[m][i][1] = o[m][i][2] = o[m][i][3] = 0.f;
-    mx[m][0] = mx[m][1] = -INFINITY;
-    l[m][0] = l[m][1] = 0.f;
+        for (int h = 0; h < HD / 64; ++h) cp_async<16>(st + (t * (HD / 64) + h) * R::kPieceK, src + 64 * h, live);
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int32_t key = key0 + 8 * (s >> 1) + 2 * j + (s & 1);
+        const bool live = key < kend;
+        cp_async<HD / 8>(ring + slot * R::kStage + R::kOffV + s * R::kPieceV + lane * (HD / 8),
+                         vb + (int64_t)(live ? key : key0) * c.ld + g * (HD / 8), live);
+      }
+      const uint32_t sc = ring + slot * R::kStage + R::kOffS + lane * 8;
+      cp_async<4>(sc, ksp + (key0 >> block_shift), true);
+      cp_async<4>(sc + 4, vsp + (key0 >> block_shift), true);
+    }
+    cp_async_commit();  // a group per stage, whether it holds anything or not
+  };
+  constexpr int kStep = 16 * kWarps;
+  const int32_t first = k0 + 16 * warp;
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) fetch(first + i * kStep, i);
+
+  uint32_t q[NT][HD / 16][2];
+  float fac[NT][2];
+  load_q_tile<HD, NT>(c, p, b, kvh, r0, g, j, q, fac);
+  // columns 2j, 2j + 1 of each row tile; rows that are not there see every key (they force no mask)
+  int32_t lim[NT][2], lim_min = kend;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t r = r0 + 8 * n + 2 * j + i;
+      lim[n][i] = r < p.n_rows ? row_limit(p, r, len) : kend;
+      lim_min = min(lim_min, lim[n][i]);
+    }
+  lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 1));
+  lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 2));
+
+  constexpr int kTiles = HD / 16;  // row tiles of O^T
+  constexpr int VW = HD / 32;      // 32-bit words of a V piece
+  float o[NT][kTiles][4];
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+    m[n][0] = m[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.f;
   }
 
-  constexpr int VW = HD / 32;  // 32-bit words of a V piece
-  for (int32_t grp = g0 + warp; grp < g1; grp += kWarps) {
-    const int32_t key0 = grp * 16;
-    KFrag<HD> kf;
-    load_k<HD>(kf, kb, c.ld, key0, kend, g, j);
-    uint32_t vw[4][VW];
+  int slot = 0;
+#pragma unroll 1
+  for (int32_t key0 = first; key0 < kend; key0 += kStep) {
+    fetch(key0 + (kRing - 1) * kStep, slot == 0 ? kRing - 1 : slot - 1);
+    cp_async_wait<kRing - 1>();  // this stage's group has landed; a lane reads its own bytes alone
+    const uint32_t st = ring + slot * R::kStage;
+    slot = slot == kRing - 1 ? 0 : slot + 1;
+    uint4 ka[HD / 64], kc[HD / 64];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int32_t key = key0 + 8 * (s >> 1) + 2 * j + (s & 1);
+    for (int h = 0; h < HD / 64; ++h) {
+      ka[h] = ld_shared16(st + h * R::kPieceK + lane * 16);
+      kc[h] = ld_shared16(st + (HD / 64 + h) * R::kPieceK + lane * 16);
+    }
+    const uint2 sc = ld_shared8(st + R::kOffS + lane * 8);
+    const float ks = __uint_as_float(sc.x);
+    float vlog, vinv;
+    scale_log2_parts(__uint_as_float(sc.y), vlog, vinv);
+
+    float s[NT][4];
+    scores<HD, NT>(s, ka, kc, q);
+    uint32_t pb[NT][2];
 #pragma unroll
-      for (int i = 0; i < VW; ++i) vw[s][i] = 0;
-      if (key < kend) {
-        const uint8_t* src = vb + (int64_t)key * c.ld + g * (HD / 8);
-        if constexpr (HD == 128) {
-          *reinterpret_cast<uint4*>(vw[s]) = __ldg(reinterpret_cast<const uint4*>(src));
-        } else {
-          *reinterpret_cast<uint2*>(vw[s]) = __ldg(reinterpret_cast<const uint2*>(src));
+    for (int n = 0; n < NT; ++n) {
+      // s[n][0], [1]: key g, columns 2j, 2j + 1; [2], [3]: key g + 8
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float f = fac[n][i] * ks;
+        s[n][i] = fmaf(s[n][i], f, vlog);
+        s[n][2 + i] = fmaf(s[n][2 + i], f, vlog);
+      }
+      if (key0 + 16 > lim_min) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (key0 + g >= lim[n][i]) s[n][i] = -INFINITY;
+          if (key0 + 8 + g >= lim[n][i]) s[n][2 + i] = -INFINITY;
         }
       }
-    }
-    const float ks = __ldg(ksp + key0 / c.block);
-    float vlog, vinv;
-    scale_log2_parts(__ldg(vsp + key0 / c.block), vlog, vinv);
-
-    float s[2][MT][4];
-    scores<HD, MT>(s[0], kf, 0, q);
-    scores<HD, MT>(s[1], kf, 1, q);
-    uint32_t a[MT][4];
+      const float t0 = fmaxf(s[n][0], s[n][2]), t1 = fmaxf(s[n][1], s[n][3]);
+      // (-inf > -inf + 7 is false: a row that has seen nothing stays where it is)
+      if (__any_sync(0xffffffffu, t0 > m[n][0] + kFollow || t1 > m[n][1] + kFollow)) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+        for (int i = 0; i < 2; ++i) {
+          float t = i ? t1 : t0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {  // row g + 8 i
-        const float f = fac[m][i] * ks;
-        float x[4];
+          for (int off = 4; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+          const float to = fmaxf(m[n][i], t);
+          const float corr = to == m[n][i] ? 1.f : ex2_approx(m[n][i] - to);  // 0 from -inf
+          m[n][i] = to;
+          l[n][i] *= corr;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int32_t key = key0 + 8 * t + 2 * j + e;
-            x[2 * t + e] = key < lim[m][i] ? fmaf(s[t][m][2 * i + e], f, vlog) : -INFINITY;
+          for (int d = 0; d < kTiles; ++d) {
+            o[n][d][i] *= corr;
+            o[n][d][2 + i] *= corr;
           }
-        float mt = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-        const float m_new = fmaxf(mx[m][i], mt);
-        if (__any_sync(0xffffffffu, m_new > mx[m][i])) {
-          const float corr = mx[m][i] == m_new ? 1.f : ex2_approx(mx[m][i] - m_new);  // 0 from -inf
-          l[m][i] *= corr;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            o[m][n][2 * i] *= corr;
-            o[m][n][2 * i + 1] *= corr;
-          }
-          mx[m][i] = m_new;
         }
-        const float mu = m_new == -INFINITY ? 0.f : m_new - kPBias;
-        float pr[4];
+      }
+      float pr[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(x[e] - mu);
-        l[m][i] = fmaf((pr[0] + pr[1]) + (pr[2] + pr[3]), vinv, l[m][i]);
-        a[m][i] = pack_f16x2(pr[0], pr[1]);
-        a[m][2 + i] = pack_f16x2(pr[2], pr[3]);
+      for (int i = 0; i < 2; ++i) {
+        const float mu = m[n][i] == -INFINITY ? 0.f : m[n][i] - kPBias;
+        pr[i] = ex2_approx(s[n][i] - mu);
+        pr[2 + i] = ex2_approx(s[n][2 + i] - mu);
+        l[n][i] = fmaf(pr[i] + pr[2 + i], vinv, l[n][i]);
+      }
+      pb[n][0] = transpose8x8(pack_f16x2(pr[0], pr[1]));
+      pb[n][1] = transpose8x8(pack_f16x2(pr[2], pr[3]));
+    }
+    uint32_t vw[4][VW];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t at = st + R::kOffV + k * R::kPieceV + lane * (HD / 8);
+      if constexpr (HD == 128) {
+        *reinterpret_cast<uint4*>(vw[k]) = ld_shared16(at);
+      } else {
+        *reinterpret_cast<uint2*>(vw[k]) = ld_shared8(at);
       }
     }
 #pragma unroll
     for (int w = 0; w < VW; ++w) {
-      // bytes 4w .. 4w+3 of the pieces of keys (0, 1) and (2, 3)
+      // bytes 4w .. 4w+3 of the pieces of keys (2j, 2j+1) and (8 + 2j, 8 + 2j + 1)
       const uint32_t lo0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), hi0 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
       const uint32_t lo1 = __byte_perm(vw[2][w], vw[3][w], 0x5140), hi1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+      const uint32_t a0 = cvt_lo(lo0), a1 = cvt_hi(lo0), a2 = cvt_lo(lo1), a3 = cvt_hi(lo1);
+      const uint32_t b0 = cvt_lo(hi0), b1 = cvt_hi(hi0), b2 = cvt_lo(hi1), b3 = cvt_hi(hi1);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        mma_f16(o[m][4 * w + 0], a[m], cvt_lo(lo0), cvt_lo(lo1));
-        mma_f16(o[m][4 * w + 1], a[m], cvt_hi(lo0), cvt_hi(lo1));
-        mma_f16(o[m][4 * w + 2], a[m], cvt_lo(hi0), cvt_lo(hi1));
-        mma_f16(o[m][4 * w + 3], a[m], cvt_hi(hi0), cvt_hi(hi1));
+      for (int n = 0; n < NT; ++n) {
+        mma_f16(o[n][2 * w], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+        mma_f16(o[n][2 * w + 1], b0, b1, b2, b3, pb[n][0], pb[n][1]);
       }
     }
   }
+  cp_async_wait<0>();
+  __syncthreads();  // the ring's memory takes the warps' parts now
 
-  // each warp's part to shared memory; accumulator column (tile i, 2j + e) is dim (2j + e) * (HD / 8) + i
+  // lane (g, j): rows 2j, 2j + 1 of each tile, dims hd/8 g + (2i, 2i + 1)
+  float* sm_o = reinterpret_cast<float*>(sm_raw);
+  float2* sm_ml = reinterpret_cast<float2*>(sm_o + kWarps * 8 * NT * R::kRowPitch);
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float lr = l[m][i];
-      lr += __shfl_xor_sync(0xffffffffu, lr, 1);
-      lr += __shfl_xor_sync(0xffffffffu, lr, 2);
-      const int row = 16 * m + 8 * i + g;
-      if (j == 0) sm_ml[warp * 16 * MT + row] = make_float2(mx[m][i], lr);
-      float* dst = sm_o + (warp * 16 * MT + row) * HD;
+      float lr = l[n][i];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int off = 4; off < 32; off <<= 1) lr += __shfl_xor_sync(0xffffffffu, lr, off);
+      const int row = warp * 8 * NT + 8 * n + 2 * j + i;
+      if (g == 0) sm_ml[row] = make_float2(m[n][i], lr);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) dst[(2 * j + e) * (HD / 8) + n] = o[m][n][2 * i + e];
+      for (int d = 0; d < kTiles; ++d)
+        *reinterpret_cast<float2*>(sm_o + row * R::kRowPitch + g * (HD / 8) + 2 * d) = make_float2(o[n][d][i], o[n][d][2 + i]);
     }
   __syncthreads();
-  // a thread joins the warps' parts of 8 columns of a row, in warp order
-  for (int u = threadIdx.x; u < 16 * MT * (HD / 8); u += 32 * kWarps) {
-    const int row = u / (HD / 8), col = (u % (HD / 8)) * 8;
+  // a thread joins the warps' parts of 4 columns of a row, in warp order
+  for (int u = threadIdx.x; u < 8 * NT * (HD / 4); u += 32 * kWarps) {
+    const int row = u / (HD / 4), col = (u % (HD / 4)) * 4;
     const int64_t r = r0 + row;
-    if (r >= p.n_rows) continue;
-    float m = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_ml[w * 16 * MT + row].x);
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, lsum = 0.f;
+    if (r >= p.n_rows) break;
+    float ref = -INFINITY, lsum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = sm_ml[w * 16 * MT + row];
-      const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - m);
-      lsum = fmaf(f, ml.y, lsum);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(f, sm_o[(w * 16 * MT + row) * HD + col + e], acc[e]);
+      const float2 ml = sm_ml[w * 8 * NT + row];
+      if (ml.y != 0.f) ref = fmaxf(ref, ml.x);
     }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 ml = sm_ml[w * 8 * NT + row];
+      const float f = ml.y == 0.f ? 0.f : ex2_approx(ml.x - ref);
+      lsum = fmaf(f, ml.y, lsum);
+      const float4 x = *reinterpret_cast<const float4*>(sm_o + (w * 8 * NT + row) * R::kRowPitch + col);
+      acc[0] = fmaf(f, x.x, acc[0]);
+      acc[1] = fmaf(f, x.y, acc[1]);
+      acc[2] = fmaf(f, x.z, acc[2]);
+      acc[3] = fmaf(f, x.w, acc[3]);
+    }
+    ref -= kPBias;
     if (p.splits > 1) {
       const int64_t pr = ((int64_t)split * c.batch * c.n_kv + blockIdx.z) * p.n_rows + r;
-      float4* dst = reinterpret_cast<float4*>(p.part_o + pr * HD + col);
-      dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-      if (col == 0) p.part_ml[pr] = make_float2(lsum == 0.f ? -INFINITY : m - kPBias, lsum);
+      *reinterpret_cast<float4*>(p.part_o + pr * HD + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (col == 0) p.part_ml[pr] = make_float2(lsum == 0.f ? -INFINITY : ref, lsum);
     } else {
       const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] *= inv;
       const int64_t qi = r / p.group;
       const int32_t h = kvh * p.group + (int32_t)(r % p.group);
       if (!dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store)) continue;
-      store_o8(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col, acc);
+      *reinterpret_cast<uint2*>(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col) =
+          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
       if (col == 0 && p.lse)
-        p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] =
-            lsum == 0.f ? -INFINITY : (m - kPBias + log2f(lsum)) * kLn2;
+        p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = lsum == 0.f ? -INFINITY : (ref + log2f(lsum)) * kLn2;
     }
   }
 }
 
-// Joins the key splits of every row, in split order; a thread has 8 columns.
+// Joins the key ranges of one row a CTA: 128 threads are 32 x 4 columns (hd 64:
+// 16 x 4) by groups that take the ranges in turn; the groups' sums are added in
+// order.
+constexpr int kMaxSplits = 256;
+
 template <int HD>
-__global__ void __launch_bounds__(256) rows_join_kernel(const Cache c, const Query p) {
+__global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ Cache c, const __grid_constant__ Query p) {
   pdl_trigger();
   pdl_wait();
-  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t rows = (int64_t)c.batch * c.n_kv * p.n_rows;
-  if (u >= rows * (HD / 8)) return;
-  const int64_t pr = u / (HD / 8);
-  const int col = (int)(u % (HD / 8)) * 8;
-  float acc[8], lse;
-  join_row<HD>(p.part_o, p.part_ml, p.splits, rows, pr, col, acc, lse);
+  constexpr int kCols = HD / 4, kGroups = 128 / kCols;
+  __shared__ float wgt[kMaxSplits];
+  __shared__ float red[2][4];
+  __shared__ float4 part[kGroups][kCols];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t rows = (int64_t)c.batch * c.n_kv * p.n_rows, pr = blockIdx.x;
+  float2 ml[kMaxSplits / 128];
+  float ref = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / 128; ++i) {
+    const int s = tid + 128 * i;
+    ml[i] = s < p.splits ? p.part_ml[s * rows + pr] : make_float2(-INFINITY, 0.f);
+    if (ml[i].y != 0.f) ref = fmaxf(ref, ml[i].x);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, off));
+  if (lane == 0) red[0][warp] = ref;
+  __syncthreads();
+  ref = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  float lsum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / 128; ++i) {
+    const float f = ml[i].y == 0.f ? 0.f : ex2_approx(ml[i].x - ref);
+    wgt[tid + 128 * i] = f;
+    lsum = fmaf(f, ml[i].y, lsum);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, off);
+  if (lane == 0) red[1][warp] = lsum;
+  __syncthreads();
+  lsum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  const int grp = tid / kCols, col = tid % kCols;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* src = p.part_o + pr * HD + col * 4;
+#pragma unroll 8
+  for (int s = grp; s < p.splits; s += kGroups) {
+    const float f = wgt[s];
+    if (f != 0.f) {  // a range that shows the row nothing wrote nothing
+      const float4 x = *reinterpret_cast<const float4*>(src + (int64_t)s * rows * HD);
+      acc.x = fmaf(f, x.x, acc.x);
+      acc.y = fmaf(f, x.y, acc.y);
+      acc.z = fmaf(f, x.z, acc.z);
+      acc.w = fmaf(f, x.w, acc.w);
+    }
+  }
+  part[grp][col] = acc;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int i = 1; i < kGroups; ++i) {
+    const float4 x = part[i][col];
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
+  }
+  const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
   const int64_t bg = pr / p.n_rows, r = pr % p.n_rows;
   const int32_t b = (int32_t)(bg / c.n_kv), kvh = (int32_t)(bg % c.n_kv);
   const int64_t qi = r / p.group;
   const int32_t h = kvh * p.group + (int32_t)(r % p.group);
   if (!dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store)) return;
-  store_o8(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col, acc);
-  if (col == 0 && p.lse) p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = lse;
+  *reinterpret_cast<uint2*>(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col * 4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (col == 0 && p.lse)
+    p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = lsum == 0.f ? -INFINITY : (ref + log2f(lsum)) * kLn2;
 }
 
 // ------------------------------------------------------------------ weighing
-// A warp owns a block of rows: it walks the query rows 16 MT at a time and sums
+// A warp owns a block of rows: it walks the query rows 8 NT at a time and sums
 // 2^(s - lse) over them and its keys, so that nothing is added by two threads.
-template <int HD, int MT>
-__global__ void __launch_bounds__(32 * kWarps) rows_weigh_kernel(const Cache c, const Query p, float decay,
+// The keys' loads (64 keys at a time) go out before the queries are laid out.
+template <int HD, int NT>
+__global__ void __launch_bounds__(32 * kWarps, 4) rows_weigh_kernel(const __grid_constant__ Cache c,
+                                                                const __grid_constant__ Query p, float decay,
                                                                 float* __restrict__ weight) {
   pdl_trigger();
   pdl_wait();
+  constexpr int kGroups = 4;  // of 16 keys, loaded together
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
   const int32_t b = blockIdx.y / c.n_kv, kvh = blockIdx.y % c.n_kv;
   const int32_t len = shown_rows(c, b, p.n_new, p.status, threadIdx.x == 0);
   const int32_t blk = (int32_t)blockIdx.x * kWarps + warp;
   const int32_t k0 = blk * c.block, k1 = min(len, k0 + c.block);
   if (k0 >= len) return;
-  const uint8_t* kb = c.k + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD;
+  const uint8_t* kb = c.k + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD + 16 * j;
   const float ks = __ldg(c.k_scale + (int64_t)blockIdx.y * c.n_blocks + blk);
+  float* w = weight + (int64_t)blockIdx.y * c.n_blocks + blk;
+  const float before = *w;
   float sum = 0.f;
-  for (int64_t r0 = 0; r0 < p.n_rows; r0 += 16 * MT) {
-    const int64_t r_last = (r0 + 16 * MT < p.n_rows ? r0 + 16 * MT : p.n_rows) - 1;
-    if (row_limit(p, r_last, len) <= k0) continue;  // the tile's last row sees the most
-    uint32_t q[MT][HD / 16][4];
-    float fac[MT][2], lse[MT][2];
-    int32_t lim[MT][2];
-    load_q_tile<HD, MT>(c, p, b, kvh, r0, g, j, q, fac);
+  for (int32_t kc = k0; kc < k1; kc += 16 * kGroups) {
+    uint4 ka[kGroups][2][HD / 64];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t r = r0 + 16 * m + 8 * i + g;
-        lim[m][i] = row_limit(p, r, len);
-        lse[m][i] = 0.f;
-        if (r < p.n_rows) {
-          const int64_t qi = r / p.group;
-          const int32_t h = kvh * p.group + (int32_t)(r % p.group);
-          lse[m][i] = p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi];
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int h = 0; h < HD / 64; ++h) {
+          const int32_t key = kc + 16 * i + 8 * t + g;
+          ka[i][t][h] = make_uint4(0, 0, 0, 0);
+          if (key < k1) ka[i][t][h] = __ldg(reinterpret_cast<const uint4*>(kb + (int64_t)key * c.ld + 64 * h));
         }
-        if (lse[m][i] == -INFINITY) lim[m][i] = 0;  // a row that saw nothing weighs nothing
-        lse[m][i] *= kLog2e;
-        fac[m][i] *= ks;
+    for (int64_t r0 = 0; r0 < p.n_rows; r0 += 8 * NT) {
+      const int64_t r_last = (r0 + 8 * NT < p.n_rows ? r0 + 8 * NT : p.n_rows) - 1;
+      if (row_limit(p, r_last, len) <= kc) continue;  // the tile's last row sees the most
+      uint32_t q[NT][HD / 16][2];
+      float fac[NT][2], lse[NT][2];
+      int32_t lim[NT][2];
+      load_q_tile<HD, NT>(c, p, b, kvh, r0, g, j, q, fac);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int64_t r = r0 + 8 * n + 2 * j + i;
+          lim[n][i] = min(k1, row_limit(p, r, len));
+          lse[n][i] = 0.f;
+          if (r < p.n_rows) {
+            const int64_t qi = r / p.group;
+            const int32_t h = kvh * p.group + (int32_t)(r % p.group);
+            lse[n][i] = p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi];
+          }
+          if (lse[n][i] == -INFINITY) lim[n][i] = 0;  // a row that saw nothing weighs nothing
+          lse[n][i] *= kLog2e;
+          fac[n][i] *= ks;
+        }
+      float part = 0.f;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        const int32_t key0 = kc + 16 * i;
+        if (key0 >= k1) break;
+        float s[NT][4];
+        scores<HD, NT>(s, ka[i][0], ka[i][1], q);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // key g + 8 (e / 2), column 2j + e % 2
+            if (key0 + 8 * (e >> 1) + g < lim[n][e & 1])
+              part += ex2_approx(fmaf(s[n][e], fac[n][e & 1], -lse[n][e & 1]));
+          }
       }
-    float part = 0.f;
-    for (int32_t key0 = k0; key0 < k1; key0 += 16) {
-      KFrag<HD> kf;
-      load_k<HD>(kf, kb, c.ld, key0, k1, g, j);
-      float s[2][MT][4];
-      scores<HD, MT>(s[0], kf, 0, q);
-      scores<HD, MT>(s[1], kf, 1, q);
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int32_t key = key0 + 8 * t + 2 * j + e;
-              if (key < lim[m][i]) part += ex2_approx(fmaf(s[t][m][2 * i + e], fac[m][i], -lse[m][i]));
-            }
+      sum += part;
     }
-    sum += part;
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (lane == 0 && dcheck(blk < c.n_blocks, p.status, kWhereKv8Store)) {
-    float* w = weight + (int64_t)blockIdx.y * c.n_blocks + blk;
-    *w = fmaf(decay, *w, sum);
+  if (lane == 0 && dcheck(blk < c.n_blocks, p.status, kWhereKv8Store)) *w = fmaf(decay, before, sum);
+}
+
+int rows_tiles(const Query& p) { return p.n_rows <= 8 ? 1 : 2; }  // row tiles of a CTA
+
+template <int HD, int NT>
+cosmot_status launch_attention(const Cache& c, const Query& p, cudaStream_t s) {
+  constexpr int smem = Ring<HD>::smem(NT);
+  static std::mutex mu;
+  static uint64_t done = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return COSMOT_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev >= 64 || !(done & (1ull << dev))) {
+      if (cudaFuncSetAttribute(rows_attention_kernel<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return COSMOT_ERR_CUDA;
+      if (dev < 64) done |= 1ull << dev;
+    }
   }
+  const dim3 grid((unsigned)p.splits, (unsigned)((p.n_rows + 8 * NT - 1) / (8 * NT)), (unsigned)(c.batch * c.n_kv));
+  return launch_status(launch_pdl(rows_attention_kernel<HD, NT>, grid, dim3(32 * kWarps), smem, s, nullptr, c, p));
 }
 
 }  // namespace
 
-int32_t rows_splits(const Cache& c, const Query& p, int32_t max_len) {
-  const int64_t tiles = (p.n_rows + 15) / 16 * c.batch * c.n_kv;
-  if (tiles <= 0) return 1;
-  const int64_t want = (2 * (int64_t)num_sms() + tiles - 1) / tiles;
-  const int64_t most = ((int64_t)max_len + 255) / 256;
-  const int64_t s = want < most ? want : most;
-  return (int32_t)(s < 1 ? 1 : (s > 512 ? 512 : s));
+void rows_plan(const Cache& c, Query& p, int32_t max_len) {
+  const int64_t per = 8 * rows_tiles(p), tiles = (p.n_rows + per - 1) / per * c.batch * c.n_kv;
+  p.splits = 1;
+  p.chunk = max_len;
+  if (tiles <= 0) return;
+  // as many key ranges as fill the SMs once (a batch of unequal lengths: four
+  // times, so that the long ones are not left alone), of 256 keys at least
+  const int64_t want = (int64_t)num_sms() * kCtasPerSm * (c.batch > 1 ? 4 : 1) / tiles;
+  int64_t n = want < 1 ? 1 : (want > kMaxSplits ? kMaxSplits : want);
+  int64_t chunk = ((max_len + n - 1) / n + 63) & ~int64_t(63);
+  if (chunk < 256) chunk = 256;
+  p.chunk = (int32_t)(chunk < INT32_MAX ? chunk : INT32_MAX);
+  p.splits = (int32_t)((max_len + chunk - 1) / chunk);
+  if (p.splits < 1) p.splits = 1;
 }
 
 cosmot_status rows_attention(const Cache& c, const Query& p, cudaStream_t s) {
-  constexpr int MT = 1;
-  const int64_t tiles = (p.n_rows + 16 * MT - 1) / (16 * MT);
-  if (tiles > 65535) return COSMOT_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)p.splits, (unsigned)tiles, (unsigned)(c.batch * c.n_kv));
-  const size_t smem = (size_t)kWarps * 16 * MT * (c.hd * 4 + 8);
-  cosmot_status st = launch_status(
-      c.hd == 128 ? launch_pdl(rows_attention_kernel<128, MT>, grid, dim3(32 * kWarps), smem, s, nullptr, c, p)
-                  : launch_pdl(rows_attention_kernel<64, MT>, grid, dim3(32 * kWarps), smem, s, nullptr, c, p));
+  const bool one = rows_tiles(p) == 1;
+  cosmot_status st;
+  if (c.hd == 128)
+    st = one ? launch_attention<128, 1>(c, p, s) : launch_attention<128, 2>(c, p, s);
+  else
+    st = one ? launch_attention<64, 1>(c, p, s) : launch_attention<64, 2>(c, p, s);
   if (st != COSMOT_OK || p.splits == 1) return st;
-  const int64_t units = (int64_t)c.batch * c.n_kv * p.n_rows * (c.hd / 8);
-  const dim3 jgrid((unsigned)((units + 255) / 256));
-  return launch_status(c.hd == 128 ? launch_pdl(rows_join_kernel<128>, jgrid, dim3(256), 0, s, nullptr, c, p)
-                                   : launch_pdl(rows_join_kernel<64>, jgrid, dim3(256), 0, s, nullptr, c, p));
+  const dim3 jgrid((unsigned)((int64_t)c.batch * c.n_kv * p.n_rows));
+  return launch_status(c.hd == 128 ? launch_pdl(rows_join_kernel<128>, jgrid, dim3(128), 0, s, nullptr, c, p)
+                                   : launch_pdl(rows_join_kernel<64>, jgrid, dim3(128), 0, s, nullptr, c, p));
 }
 
 cosmot_status rows_weigh(const Cache& c, const Query& p, float decay, float* weight, cudaStream_t s) {
