@@ -6,52 +6,58 @@ namespace cosmot {
 namespace kv8 {
 
 // ------------------------------------------------------------------ store
-// One CTA per (block of rows, sequence x head, K or V).  Each thread owns
-// kUnits units of 16 elements: 32 bytes read, 16 written.  The block's largest
-// magnitude is reduced over the CTA, then the elements, still in registers,
-// are rounded against the scale, so every input byte is read once.  Rows of
-// the block that were there before are read only if the scale grows.
+// One CTA per (block of rows, sequence x head, K or V), the heads of a block one
+// after another, so that CTAs that run together read whole rows.  Each thread
+// owns kUnits pieces of 8 elements: 16 bytes read, 8 written, neighbours side by
+// side.  The block's largest magnitude is reduced over the CTA, then the
+// elements, still in registers, are rounded against the scale, so every input
+// byte is read once.  Rows of the block that were there before are read only if
+// the scale grows.
 // bound: HBM (4 bytes read and 2 written for each K and V element).
+constexpr int kStoreThreads = 256;
+
 template <int kUnits>
-__global__ void __launch_bounds__(256) store_kernel(const Cache c, const __nv_bfloat16* __restrict__ ksrc,
-                                                    const __nv_bfloat16* __restrict__ vsrc, int64_t ld_src,
-                                                    int64_t src_bstride, int32_t n, int* status) {
+__global__ void __launch_bounds__(kStoreThreads, 3)
+    store_kernel(const __grid_constant__ Cache c, const __nv_bfloat16* __restrict__ ksrc,
+                 const __nv_bfloat16* __restrict__ vsrc, int64_t ld_src, int64_t src_bstride, int32_t n, int* status) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float part[8];
-  const int32_t b = blockIdx.y / c.n_kv, g = blockIdx.y % c.n_kv;
+  __shared__ float part[kStoreThreads / 32];
+  const uint32_t sides = 2u * c.batch * c.n_kv;  // K and V of every head
+  const uint32_t side = blockIdx.x % sides;
+  const bool is_v = side & 1;
+  const int32_t bg = side >> 1, b = bg / c.n_kv, g = bg % c.n_kv;
   const int32_t held = c.lens[b];
   if (held < 0 || held > c.capacity - n) {
     if (threadIdx.x == 0) latch_status(status, COSMOT_ERR_BOUNDS, kWhereKv8Lens);
     return;
   }
-  const int32_t blk = held / c.block + (int32_t)blockIdx.x;
+  const int32_t blk = held / c.block + (int32_t)(blockIdx.x / sides);
   const int32_t row0 = blk * c.block, end = held + n;
   if (row0 >= end) return;
-  const bool is_v = blockIdx.z != 0;
-  const __nv_bfloat16* src = (is_v ? vsrc : ksrc) + (int64_t)b * src_bstride * ld_src + (int64_t)g * c.hd;
-  uint8_t* dst = (is_v ? c.v : c.k) + (int64_t)b * c.bstride * c.ld + (int64_t)g * c.hd;
-  float* scale = (is_v ? c.v_scale : c.k_scale) + (int64_t)blockIdx.y * c.n_blocks + blk;
-  const int per_row = c.hd >> 4;  // units a row
+  const int per_row = c.hd >> 3;  // pieces a row
+  const int step = (int)blockDim.x / per_row;
+  const int32_t first = row0 + (int32_t)threadIdx.x / per_row;
+  const int col = ((int)threadIdx.x % per_row) * 8;
+  const __nv_bfloat16* src =
+      (is_v ? vsrc : ksrc) + ((int64_t)b * src_bstride + (first - held)) * ld_src + (int64_t)g * c.hd + col;
+  uint8_t* dst = (is_v ? c.v : c.k) + ((int64_t)b * c.bstride + first) * c.ld + (int64_t)g * c.hd + col;
+  float* scale = (is_v ? c.v_scale : c.k_scale) + (int64_t)bg * c.n_blocks + blk;
 
-  uint4 x[kUnits][2];
+  uint4 x[kUnits];
   float amax = 0.f;
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
-    const int unit = (int)threadIdx.x + u * (int)blockDim.x;
-    const int32_t row = row0 + unit / per_row;
-    x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
-    if (row >= held && row < end) {
-      const uint4* p = reinterpret_cast<const uint4*>(src + (int64_t)(row - held) * ld_src + (unit % per_row) * 16);
-      x[u][0] = __ldg(p);
-      x[u][1] = __ldg(p + 1);
-    }
+    const int32_t row = first + u * step;
+    x[u] = make_uint4(0, 0, 0, 0);
+    if (row >= held && row < end) x[u] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(u * step) * ld_src));
   }
+  const float old = row0 < held ? *scale : 0.f;  // read by every thread before thread 0 writes it
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(x[u]);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[u]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const float2 f = unpack_bf16x2(w[i]);
       // infinities saturate like any other large value and NaN stays NaN: neither sets the scale
       const float a = fabsf(f.x), d = fabsf(f.y);
@@ -62,7 +68,6 @@ __global__ void __launch_bounds__(256) store_kernel(const Cache c, const __nv_bf
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
-  const float old = row0 < held ? *scale : 0.f;  // read by every thread before thread 0 writes it
   __syncthreads();
   for (int i = 0; i < (int)blockDim.x >> 5; ++i) amax = fmaxf(amax, part[i]);
   const float fresh = exp2_int(scale_exponent(amax));
@@ -73,24 +78,23 @@ __global__ void __launch_bounds__(256) store_kernel(const Cache c, const __nv_bf
   if (threadIdx.x == 0 && dcheck(blk < c.n_blocks, status, kWhereKv8Store)) *scale = now;
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
-    const int unit = (int)threadIdx.x + u * (int)blockDim.x;
-    const int32_t row = row0 + unit / per_row;
+    const int32_t row = first + u * step;
     if (row >= end || (row < held && !again)) continue;
-    uint4* out = reinterpret_cast<uint4*>(dst + (int64_t)row * c.ld + (unit % per_row) * 16);
-    uint32_t y[4];
+    uint2* out = reinterpret_cast<uint2*>(dst + (int64_t)(u * step) * c.ld);
+    uint32_t y[2];
     if (row >= held) {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(x[u]);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[u]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const float2 f0 = unpack_bf16x2(w[2 * i]), f1 = unpack_bf16x2(w[2 * i + 1]);
         y[i] = (uint32_t)f32x2_to_e4m3x2(f0.x * inv, f0.y * inv) |
                ((uint32_t)f32x2_to_e4m3x2(f1.x * inv, f1.y * inv) << 16);
       }
     } else {
-      const uint4 o4 = *out;
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(&o4);
+      const uint2 o2 = *out;
+      const uint32_t w[2] = {o2.x, o2.y};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const uint32_t a = cvt_lo(w[i]), d = cvt_hi(w[i]);
         const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&a));
         const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&d));
@@ -98,15 +102,17 @@ __global__ void __launch_bounds__(256) store_kernel(const Cache c, const __nv_bf
                ((uint32_t)f32x2_to_e4m3x2(f1.x * old * inv, f1.y * old * inv) << 16);
       }
     }
-    if (dcheck(row < c.capacity, status, kWhereKv8Store)) *out = make_uint4(y[0], y[1], y[2], y[3]);
+    if (dcheck(row < c.capacity, status, kWhereKv8Store)) *out = make_uint2(y[0], y[1]);
   }
 }
 
 // ------------------------------------------------------------------ evict
 // Two kernels.  The first, one CTA per (sequence, head), finds which blocks
-// stay: a radix select over the ordered bits of the weights (four passes of 8
-// bits), then one pass in index order that keeps what is above the threshold,
-// the first ones equal to it, and the fixed blocks.  The second moves them.
+// stay.  Up to kSelectThreads free blocks every thread counts the blocks that
+// come before its own (one pass over shared memory); above, a radix select over
+// the ordered bits of the weights (four passes of 8 bits) gives the threshold.
+// Then one pass in index order lists the blocks that stay.  The second kernel
+// moves them.
 constexpr int kSelectThreads = 512;
 
 struct EvictPlan {  // per sequence, in the workspace
@@ -127,6 +133,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cach
   pdl_trigger();
   pdl_wait();
   __shared__ uint32_t hist[256];
+  __shared__ uint32_t keys[kSelectThreads];
   __shared__ uint32_t sh_prefix, sh_need;
   __shared__ uint32_t warp_cnt[2][kSelectThreads / 32];
   const int32_t b = blockIdx.x / c.n_kv;
@@ -145,7 +152,21 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cach
   // threshold: the (count - n_fixed)-th largest key of [head, tail)
   uint32_t prefix = 0, need = (uint32_t)(count - n_fixed);
   const bool all = (int32_t)need >= tail - head;
-  if (!all && need > 0) {
+  const bool count_ranks = !all && need > 0 && tail - head <= kSelectThreads;
+  if (count_ranks) {
+    const bool mine = tid < tail - head;
+    const uint32_t k = mine ? weight_key(w[head + tid]) : 0u;
+    keys[tid] = k;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int i = 0; i < tail - head; ++i) {
+      const uint32_t x = keys[i];
+      before += x > k || (x == k && i < tid) ? 1u : 0u;
+    }
+    __syncthreads();
+    keys[tid] = mine && before < need ? 1u : 0u;  // block head + tid is among the first `need`
+    __syncthreads();
+  } else if (!all && need > 0) {
     for (int shift = 24; shift >= 0; shift -= 8) {
       for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
       __syncthreads();
@@ -186,7 +207,9 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cach
   for (int32_t j0 = 0; j0 < nb; j0 += kSelectThreads) {
     const int32_t j = j0 + tid;
     bool sure = j < nb && (j < head || j >= tail || all), tie = false;
-    if (j < nb && !sure && count > n_fixed) {
+    if (count_ranks) {
+      sure = sure || (j >= head && j < tail && keys[j - head] != 0);
+    } else if (j < nb && !sure && count > n_fixed) {
       const uint32_t k = weight_key(w[j]);
       sure = k > prefix;
       tie = k == prefix;
@@ -219,13 +242,14 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cach
 
 // Blocks move towards the front: the source of the j-th kept block is list[j]
 // >= j, ascending.  A thread owns one 16-byte piece of one row of every block
-// and walks j upwards; it reads list[j + 1], ... before it writes block j, and
-// no later source is a block that it has written, so the move is in place
-// without any thread waiting for another.  Slice z = 2 moves the scales and the
-// weights in the same order and writes the length.
-constexpr int kMoveAhead = 8;
+// and walks j upwards; it reads sources of blocks j and later before it writes
+// block j, and no later source is a block that it has written, so the move is in
+// place without any thread waiting for another.  Two batches of kMoveAhead
+// pieces: one is read while the other is written.  Slice z = 2 moves the scales
+// and the weights in the same order and writes the length.
+constexpr int kMoveAhead = 8, kMoveThreads = 64;
 
-__global__ void __launch_bounds__(256) evict_move_kernel(const Cache c, const EvictPlan* __restrict__ plan,
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ Cache c, const EvictPlan* __restrict__ plan,
                                                          const int32_t* __restrict__ list, const float* weight,
                                                          float* weight_out, int32_t* lens_out, int* status) {
   pdl_trigger();
@@ -236,20 +260,28 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const Cache c, const Ev
   if (blockIdx.z == 2) {
     if (blockIdx.x != 0) return;
     const int64_t base = (int64_t)blockIdx.y * c.n_blocks;
-    for (int32_t j0 = 0; j0 < pl.count; j0 += (int32_t)blockDim.x) {
-      const int32_t j = j0 + (int32_t)threadIdx.x;
-      float ks = 0.f, vs = 0.f, w = 0.f;
-      if (j < pl.count) {
-        const int32_t s = src[j];
-        ks = c.k_scale[base + s];
-        vs = c.v_scale[base + s];
-        w = weight[base + s];
+    // sources lie at or behind their destinations: a chunk is read whole before it is written
+    for (int32_t j0 = 0; j0 < pl.count; j0 += kMoveAhead * kMoveThreads) {
+      float ks[kMoveAhead], vs[kMoveAhead], w[kMoveAhead];
+#pragma unroll
+      for (int i = 0; i < kMoveAhead; ++i) {
+        const int32_t j = j0 + i * kMoveThreads + (int32_t)threadIdx.x;
+        if (j < pl.count) {
+          const int32_t s = src[j];
+          ks[i] = c.k_scale[base + s];
+          vs[i] = c.v_scale[base + s];
+          w[i] = weight[base + s];
+        }
       }
       __syncthreads();
-      if (j < pl.count && dcheck(j < c.n_blocks, status, kWhereKv8Store)) {
-        c.k_scale[base + j] = ks;
-        c.v_scale[base + j] = vs;
-        weight_out[base + j] = w;
+#pragma unroll
+      for (int i = 0; i < kMoveAhead; ++i) {
+        const int32_t j = j0 + i * kMoveThreads + (int32_t)threadIdx.x;
+        if (j < pl.count && dcheck(j < c.n_blocks, status, kWhereKv8Store)) {
+          c.k_scale[base + j] = ks[i];
+          c.v_scale[base + j] = vs[i];
+          weight_out[base + j] = w[i];
+        }
       }
     }
     __syncthreads();
@@ -279,21 +311,25 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const Cache c, const Ev
     else
       lo = mid + 1;
   }
-  for (int32_t j = lo; j < pl.count; j += kMoveAhead) {
-    uint4 x[kMoveAhead];
-    bool live[kMoveAhead];
-#pragma unroll
-    for (int i = 0; i < kMoveAhead; ++i) {
-      live[i] = false;
-      if (j + i < pl.count) {
-        const int32_t s = src[j + i];
-        live[i] = s * c.block + r < pl.len;
-        if (live[i]) x[i] = *reinterpret_cast<const uint4*>(base + s * step);
-      }
-    }
+  // only the last block may lack the row
+  const int32_t end = pl.count - (pl.count > 0 && src[pl.count - 1] * c.block + r >= pl.len ? 1 : 0);
+  uint4 x[2][kMoveAhead];
+  auto read = [&](uint4 (&y)[kMoveAhead], int32_t j) {
 #pragma unroll
     for (int i = 0; i < kMoveAhead; ++i)
-      if (live[i]) *reinterpret_cast<uint4*>(base + (j + i) * step) = x[i];
+      if (j + i < end) y[i] = *reinterpret_cast<const uint4*>(base + __ldg(src + j + i) * step);
+  };
+  auto write = [&](const uint4 (&y)[kMoveAhead], int32_t j) {
+#pragma unroll
+    for (int i = 0; i < kMoveAhead; ++i)
+      if (j + i < end) *reinterpret_cast<uint4*>(base + (j + i) * step) = y[i];
+  };
+  read(x[0], lo);
+  for (int32_t j = lo; j < end; j += 2 * kMoveAhead) {
+    read(x[1], j + kMoveAhead);
+    write(x[0], j);
+    read(x[0], j + 2 * kMoveAhead);
+    write(x[1], j + kMoveAhead);
   }
 }
 
@@ -393,20 +429,20 @@ extern "C" cosmot_status cosmot_kv8_store(const cosmot_kv8_cache* cache, const v
   if (n_rows == 0) return COSMOT_OK;
   int* status = device_status_ptr();
   if (!status) return COSMOT_ERR_CUDA;
-  const int units = c.block * c.hd / 16;  // 64 .. 1024
-  const dim3 grid((unsigned)(((int64_t)n_rows + 2 * c.block - 2) / c.block), (unsigned)(c.batch * c.n_kv), 2);
-  const dim3 block((unsigned)(units < 256 ? units : 256));
+  const int pieces = c.block * c.hd / 8;  // 128 .. 2048
+  const int64_t ctas = 2 * (int64_t)c.batch * c.n_kv * (((int64_t)n_rows + 2 * c.block - 2) / c.block);
+  if (ctas > INT32_MAX) return COSMOT_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)ctas);
+  const dim3 block((unsigned)(pieces < kv8::kStoreThreads ? pieces : kv8::kStoreThreads));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int64_t bs = c.batch > 1 ? src_batch_stride : 0;
   const auto* ks = static_cast<const __nv_bfloat16*>(k);
   const auto* vs = static_cast<const __nv_bfloat16*>(v);
-  cudaError_t e;
-  if (units <= 256)
-    e = launch_pdl(kv8::store_kernel<1>, grid, block, 0, s, nullptr, c, ks, vs, ld_src, bs, n_rows, status);
-  else if (units == 512)
-    e = launch_pdl(kv8::store_kernel<2>, grid, block, 0, s, nullptr, c, ks, vs, ld_src, bs, n_rows, status);
-  else
-    e = launch_pdl(kv8::store_kernel<4>, grid, block, 0, s, nullptr, c, ks, vs, ld_src, bs, n_rows, status);
+  auto* kern = pieces <= 256    ? kv8::store_kernel<1>
+               : pieces == 512  ? kv8::store_kernel<2>
+               : pieces == 1024 ? kv8::store_kernel<4>
+                                : kv8::store_kernel<8>;
+  const cudaError_t e = launch_pdl(kern, grid, block, 0, s, nullptr, c, ks, vs, ld_src, bs, n_rows, status);
   return launch_status(e);
 }
 
@@ -479,7 +515,7 @@ extern "C" cosmot_status cosmot_kv8_weigh(const cosmot_kv8_cache* cache, const c
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return kv8::use_tiles(p) && p.group <= 128
              ? kv8::tile_weigh(c, p, decay, weight, kv8::bound_len(cache, query), s)
-             : kv8::rows_weigh(c, p, decay, weight, s);
+             : kv8::rows_weigh(c, p, decay, weight, kv8::bound_len(cache, query), s);
 }
 
 extern "C" cosmot_status cosmot_kv8_evict_workspace(const cosmot_kv8_cache* cache, size_t* bytes) {
@@ -511,8 +547,9 @@ extern "C" cosmot_status cosmot_kv8_evict(const cosmot_kv8_cache* cache, const f
                                 dim3(kv8::kSelectThreads), 0, s, nullptr, c, weight, keep_blocks, first_rows, last_rows,
                                 plan, list, status));
   if (st != COSMOT_OK) return st;
-  const unsigned slices = (unsigned)((c.block * c.hd / 16 + 255) / 256);
-  return launch_status(launch_pdl(kv8::evict_move_kernel, dim3(slices, (unsigned)(c.batch * c.n_kv), 3), dim3(256), 0, s,
+  const unsigned slices = (unsigned)(c.block * c.hd / 16 / kv8::kMoveThreads);  // 64 .. 1024 pieces
+  return launch_status(launch_pdl(kv8::evict_move_kernel, dim3(slices, (unsigned)(c.batch * c.n_kv), 3),
+                                  dim3(kv8::kMoveThreads), 0, s,
                                   nullptr, c, (const kv8::EvictPlan*)plan, (const int32_t*)list, weight, weight_out,
                                   lens_out, status));
 }

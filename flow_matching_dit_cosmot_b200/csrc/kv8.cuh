@@ -161,7 +161,7 @@ cosmot_status make_cache(const cosmot_kv8_cache* c, Cache& out);
 cosmot_status make_query(const cosmot_kv8_cache* c, const cosmot_kv8_query* d, Query& out);
 // Register-tile kernels (kv8_rows.cu): few packed rows.
 cosmot_status rows_attention(const Cache& c, const Query& p, cudaStream_t s);
-cosmot_status rows_weigh(const Cache& c, const Query& p, float decay, float* weight, cudaStream_t s);
+cosmot_status rows_weigh(const Cache& c, const Query& p, float decay, float* weight, int32_t max_len, cudaStream_t s);
 // Sets the key split of a register-tile attention call.
 void rows_plan(const Cache& c, Query& p, int32_t max_len);
 // tcgen05 kernels (kv8_tile.cu): many packed rows.  max_len: what the host

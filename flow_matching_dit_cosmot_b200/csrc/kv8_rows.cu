@@ -486,83 +486,122 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ weighing
-// A warp owns a block of rows: it walks the query rows 8 NT at a time and sums
-// 2^(s - lse) over them and its keys, so that nothing is added by two threads.
-// The keys' loads (64 keys at a time) go out before the queries are laid out.
+// A warp owns whole blocks of rows and sums 2^(s - lse) over their keys and
+// eight NT query rows, so that nothing is added by two threads.  The keys, the
+// blocks' scales and their old weights come through a ring of 16-key stages, as
+// above.  More query rows take more passes over the keys (from L2).
+constexpr int kWeighRing = 5;
+
+template <int HD>
+struct WeighRing {
+  static constexpr int kOffS = 2 * (HD / 64) * 512;  // ks and the old weight: 4 bytes a lane each
+  static constexpr int kStage = kOffS + 256;
+  static constexpr int kSmem = kWarps * kWeighRing * kStage;
+};
+
 template <int HD, int NT>
-__global__ void __launch_bounds__(32 * kWarps, 4) rows_weigh_kernel(const __grid_constant__ Cache c,
+__global__ void __launch_bounds__(32 * kWarps) rows_weigh_kernel(const __grid_constant__ Cache c,
                                                                 const __grid_constant__ Query p, float decay,
                                                                 float* __restrict__ weight) {
   pdl_trigger();
   pdl_wait();
-  constexpr int kGroups = 4;  // of 16 keys, loaded together
+  using R = WeighRing<HD>;
+  extern __shared__ __align__(16) uint8_t sm_raw[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
   const int32_t b = blockIdx.y / c.n_kv, kvh = blockIdx.y % c.n_kv;
   const int32_t len = shown_rows(c, b, p.n_new, p.status, threadIdx.x == 0);
-  const int32_t blk = (int32_t)blockIdx.x * kWarps + warp;
-  const int32_t k0 = blk * c.block, k1 = min(len, k0 + c.block);
-  if (k0 >= len) return;
+  // blocks blk0 + warp, + kWarps, ... of this CTA's p.chunk keys (a whole number of blocks)
+  const int32_t per = p.chunk / c.block, blk0 = (int32_t)blockIdx.x * per + warp;
+  const int32_t blk1 = min((len + c.block - 1) / c.block, ((int32_t)blockIdx.x + 1) * per);
+  if (blk0 >= blk1) return;
+  const int stages = c.block >> 4, n = ((blk1 - blk0 + kWarps - 1) / kWarps) * stages;  // stages of 16 keys
+  const int shift = 31 - __clz(stages);
   const uint8_t* kb = c.k + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD + 16 * j;
-  const float ks = __ldg(c.k_scale + (int64_t)blockIdx.y * c.n_blocks + blk);
-  float* w = weight + (int64_t)blockIdx.y * c.n_blocks + blk;
-  const float before = *w;
-  float sum = 0.f;
-  for (int32_t kc = k0; kc < k1; kc += 16 * kGroups) {
-    uint4 ka[kGroups][2][HD / 64];
+  const float* ksp = c.k_scale + (int64_t)blockIdx.y * c.n_blocks;
+  float* wp = weight + (int64_t)blockIdx.y * c.n_blocks;
+  const uint32_t ring = smem_u32(sm_raw) + warp * kWeighRing * R::kStage;
+
+  auto fetch = [&](int t, int slot) {
+    if (t < n) {
+      const int32_t blk = blk0 + (t >> shift) * kWarps, key0 = blk * c.block + (t & (stages - 1)) * 16;
+      const uint32_t st = ring + slot * R::kStage + lane * 16;
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i)
+      for (int i = 0; i < 2; ++i) {
+        const int32_t key = key0 + 8 * i + g;
+        const bool live = key < len;
+        const uint8_t* src = kb + (int64_t)(live ? key : blk * c.block) * c.ld;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int h = 0; h < HD / 64; ++h) {
-          const int32_t key = kc + 16 * i + 8 * t + g;
-          ka[i][t][h] = make_uint4(0, 0, 0, 0);
-          if (key < k1) ka[i][t][h] = __ldg(reinterpret_cast<const uint4*>(kb + (int64_t)key * c.ld + 64 * h));
-        }
-    for (int64_t r0 = 0; r0 < p.n_rows; r0 += 8 * NT) {
-      const int64_t r_last = (r0 + 8 * NT < p.n_rows ? r0 + 8 * NT : p.n_rows) - 1;
-      if (row_limit(p, r_last, len) <= kc) continue;  // the tile's last row sees the most
-      uint32_t q[NT][HD / 16][2];
-      float fac[NT][2], lse[NT][2];
-      int32_t lim[NT][2];
-      load_q_tile<HD, NT>(c, p, b, kvh, r0, g, j, q, fac);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int64_t r = r0 + 8 * n + 2 * j + i;
-          lim[n][i] = min(k1, row_limit(p, r, len));
-          lse[n][i] = 0.f;
-          if (r < p.n_rows) {
-            const int64_t qi = r / p.group;
-            const int32_t h = kvh * p.group + (int32_t)(r % p.group);
-            lse[n][i] = p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi];
-          }
-          if (lse[n][i] == -INFINITY) lim[n][i] = 0;  // a row that saw nothing weighs nothing
-          lse[n][i] *= kLog2e;
-          fac[n][i] *= ks;
-        }
-      float part = 0.f;
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        const int32_t key0 = kc + 16 * i;
-        if (key0 >= k1) break;
-        float s[NT][4];
-        scores<HD, NT>(s, ka[i][0], ka[i][1], q);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {  // key g + 8 (e / 2), column 2j + e % 2
-            if (key0 + 8 * (e >> 1) + g < lim[n][e & 1])
-              part += ex2_approx(fmaf(s[n][e], fac[n][e & 1], -lse[n][e & 1]));
-          }
+        for (int h = 0; h < HD / 64; ++h) cp_async<16>(st + (i * (HD / 64) + h) * 512, src + 64 * h, live);
       }
-      sum += part;
+      const uint32_t sc = ring + slot * R::kStage + R::kOffS + lane * 8;
+      cp_async<4>(sc, ksp + blk, true);
+      cp_async<4>(sc + 4, wp + blk, true);
+    }
+    cp_async_commit();
+  };
+
+  for (int64_t r0 = 0; r0 == 0 || r0 < p.n_rows; r0 += 8 * NT) {
+#pragma unroll
+    for (int i = 0; i < kWeighRing - 1; ++i) fetch(i, i);
+    uint32_t q[NT][HD / 16][2];
+    float fac[NT][2], lse[NT][2];
+    int32_t lim[NT][2], lim_min = len;
+    load_q_tile<HD, NT>(c, p, b, kvh, r0, g, j, q, fac);
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t r = r0 + 8 * m + 2 * j + i;
+        lim[m][i] = len;
+        lse[m][i] = INFINITY;  // rows that are not there: 2^-inf
+        if (r < p.n_rows) {
+          const int64_t qi = r / p.group;
+          const int32_t h = kvh * p.group + (int32_t)(r % p.group);
+          lse[m][i] = p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] * kLog2e;
+          lim[m][i] = lse[m][i] == -INFINITY ? 0 : row_limit(p, r, len);  // a row that saw nothing weighs nothing
+        }
+        lim_min = min(lim_min, lim[m][i]);
+      }
+    lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 1));
+    lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 2));
+    float sum = 0.f;
+    int slot = 0;
+#pragma unroll 1
+    for (int t = 0; t < n; ++t) {
+      fetch(t + kWeighRing - 1, slot == 0 ? kWeighRing - 1 : slot - 1);
+      cp_async_wait<kWeighRing - 1>();
+      const uint32_t st = ring + slot * R::kStage;
+      slot = slot == kWeighRing - 1 ? 0 : slot + 1;
+      uint4 ka[HD / 64], kc[HD / 64];
+#pragma unroll
+      for (int h = 0; h < HD / 64; ++h) {
+        ka[h] = ld_shared16(st + h * 512 + lane * 16);
+        kc[h] = ld_shared16(st + (HD / 64 + h) * 512 + lane * 16);
+      }
+      const uint2 sc = ld_shared8(st + R::kOffS + lane * 8);
+      const float ks = __uint_as_float(sc.x);
+      const int32_t blk = blk0 + (t >> shift) * kWarps, key0 = blk * c.block + (t & (stages - 1)) * 16;
+      float s[NT][4];
+      scores<HD, NT>(s, ka, kc, q);
+      const bool masked = key0 + 16 > lim_min;
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // key g + 8 (e / 2), column 2j + e % 2
+          const float x = ex2_approx(fmaf(s[m][e], fac[m][e & 1] * ks, -lse[m][e & 1]));
+          sum += masked && key0 + 8 * (e >> 1) + g >= lim[m][e & 1] ? 0.f : x;
+        }
+      if ((t & (stages - 1)) == stages - 1) {  // the block's last keys
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        // (a later pass reads what lane 0 wrote here itself: through its own copy)
+        if (lane == 0 && dcheck(blk < c.n_blocks, p.status, kWhereKv8Store))
+          wp[blk] = r0 == 0 ? fmaf(decay, __uint_as_float(sc.y), sum) : wp[blk] + sum;
+        sum = 0.f;
+      }
     }
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (lane == 0 && dcheck(blk < c.n_blocks, p.status, kWhereKv8Store)) *w = fmaf(decay, before, sum);
+  cp_async_wait<0>();
 }
 
 int rows_tiles(const Query& p) { return p.n_rows <= 8 ? 1 : 2; }  // row tiles of a CTA
@@ -617,11 +656,19 @@ cosmot_status rows_attention(const Cache& c, const Query& p, cudaStream_t s) {
                                    : launch_pdl(rows_join_kernel<64>, jgrid, dim3(128), 0, s, nullptr, c, p));
 }
 
-cosmot_status rows_weigh(const Cache& c, const Query& p, float decay, float* weight, cudaStream_t s) {
-  const dim3 grid((unsigned)((c.n_blocks + kWarps - 1) / kWarps), (unsigned)(c.batch * c.n_kv));
-  return launch_status(
-      c.hd == 128 ? launch_pdl(rows_weigh_kernel<128, 1>, grid, dim3(32 * kWarps), 0, s, nullptr, c, p, decay, weight)
-                  : launch_pdl(rows_weigh_kernel<64, 1>, grid, dim3(32 * kWarps), 0, s, nullptr, c, p, decay, weight));
+cosmot_status rows_weigh(const Cache& c, const Query& p0, float decay, float* weight, int32_t max_len, cudaStream_t s) {
+  Query p = p0;
+  // CTAs for eight warps' worth of work an SM and sub-partition, of one block a warp at least
+  const int64_t heads = (int64_t)c.batch * c.n_kv, want = (int64_t)num_sms() * 16 / heads;
+  const int64_t span = (int64_t)kWarps * c.block;
+  int64_t chunk = max_len / (want < 1 ? 1 : want) / span * span;
+  if (chunk < span) chunk = span;
+  p.chunk = (int32_t)chunk;
+  const dim3 grid((unsigned)((c.capacity + chunk - 1) / chunk), (unsigned)heads);
+  return launch_status(c.hd == 128 ? launch_pdl(rows_weigh_kernel<128, 1>, grid, dim3(32 * kWarps), WeighRing<128>::kSmem, s,
+                                                nullptr, c, p, decay, weight)
+                                   : launch_pdl(rows_weigh_kernel<64, 1>, grid, dim3(32 * kWarps), WeighRing<64>::kSmem, s,
+                                                nullptr, c, p, decay, weight));
 }
 
 }  // namespace kv8
