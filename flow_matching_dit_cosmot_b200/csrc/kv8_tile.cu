@@ -54,11 +54,15 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* status, int where) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, where));
+}
+
 // ------------------------------------------------------------------ attention
-// Registers: 128 threads x (kRegsMma + kRegsConv) + 256 x kRegsSoftmax must not
-// exceed the launch's pool (the launch checks it).
+// Registers: 256 threads x (kRegsIo + kRegsSoftmax) must not exceed the launch's pool (the launch checks it).
 constexpr int kAttnThreads = 512;
-constexpr int kRegsMma = 48, kRegsConv = 80, kRegsSoftmax = 192;
+constexpr int kRegsIo = 80, kRegsSoftmax = 176;
+constexpr int kConvWarps = 7;
 
 struct TilePlan {
   int32_t pairs;    // pairs of query tiles of a (sequence, key head)
@@ -69,15 +73,17 @@ struct TilePlan {
 
 template <int HD>
 struct AttnCfg {
-  static constexpr int kBoxes = HD / 64;
   static constexpr int kTileBytes = kTile * HD * 2;
   static constexpr int kScaleBytes = 4 * 8 * 16;  // four key tiles in flight, eight groups each
   static constexpr int kSmem = (2 + kSlots) * kTileBytes + 256 + kScaleBytes + 1024;
   static constexpr uint32_t kIdescS = idesc_f16_f32(kTile, kTile, false);
   static constexpr uint32_t kIdescO = idesc_f16_f32(kTile, HD, true);
+  __device__ static constexpr uint32_t s_col(int t) { return (uint32_t)t * 128u; }
+  __device__ static constexpr uint32_t o_col(int t) { return 256u + (uint32_t)t * HD; }
 };
 
-template <int HD>
+// NG: groups of keys with their own scale in a key tile, 128 / block.
+template <int HD, int NG>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     tile_attention_kernel(const __grid_constant__ Cache c, const __grid_constant__ Query p,
                           const __grid_constant__ TilePlan plan) {
@@ -95,7 +101,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const uint32_t bar_p_full = bar_p_half + 16;            // [2] P of keys 64-127 written
   const uint32_t bar_o_done = bar_p_full + 16;            // [1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 1 + 2 * kSlots + 7);
-  float4* scales = reinterpret_cast<float4*>(smem + (2 + kSlots) * C::kTileBytes + 256);  // [4][8] (ks, log2 vs, 1/vs)
+  // [4][NG] (ks, log2 vs, 1/vs)
+  float4* scales = reinterpret_cast<float4*>(smem + (2 + kSlots) * C::kTileBytes + 256);
+  constexpr int kGroupKeys = kTile / NG;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // work item: the pairs of all heads in turn (causal: the longest first)
@@ -114,7 +122,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(bar_q, 8);
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(bar_kv_full + 8 * s, 4);
+      mbar_init(bar_kv_full + 8 * s, kConvWarps);
       mbar_init(bar_kv_empty + 8 * s, 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -142,39 +150,41 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  const uint32_t s_col[2] = {0u, 128u}, o_col[2] = {256u, 256u + HD};
 
-  if (warp < 4) {
-    setmaxnreg_dec<kRegsMma>();
-    if (warp == 0 && lane == 0 && n_vis > 0) {
+  if (warp < 8) {
+    setmaxnreg_dec<kRegsIo>();
+    if (warp == 0) {
+    // The whole warp walks the loop and one lane issues: with uniform control flow
+    // the operands stay in uniform registers.
+    if (n_vis > 0) {
+      const uint32_t leader = elect_one();
       auto issue_s = [&](int t, int slot) {
-        const uint32_t qa = sQ + t * C::kTileBytes, ka = sKV + slot * C::kTileBytes;
+        const uint32_t qa = sw128_desc_lo(sQ + t * C::kTileBytes, 16), ka = sw128_desc_lo(sKV + slot * C::kTileBytes, 16);
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k) {
-          const uint32_t off = (k >> 2) * kBoxBytes + (k & 3) * 32;
-          umma_ss(tmem_base + s_col[t], sw128_desc(qa + off, 16, 1024), sw128_desc(ka + off, 16, 1024), C::kIdescS,
-                  k > 0 ? 1u : 0u);
+          const uint32_t off = ((k >> 2) * kBoxBytes + (k & 3) * 32) >> 4;
+          umma_ss_lo(leader, tmem_base + C::s_col(t), qa + off, ka + off, C::kIdescS, k > 0 ? 1u : 0u);
         }
       };
       auto issue_pv = [&](int t, int slot, bool acc, int half) {  // keys 64 half .. 64 half + 63
-        const uint32_t va = sKV + slot * C::kTileBytes;
+        const uint32_t va = sw128_desc_lo(sKV + slot * C::kTileBytes, kBoxBytes);
 #pragma unroll
-        for (int k = 4 * half; k < 4 * half + 4; ++k)
-          umma_ts(tmem_base + o_col[t], tmem_base + s_col[t] + 8 * k, sw128_desc(va + 2048 * k, kBoxBytes, 1024),
-                  C::kIdescO, (acc || k > 0) ? 1u : 0u);
+        for (int k = 4 * half; k < 4 * half + 4; ++k)  // 16 keys: two 8-row swizzle atoms = 2048 bytes
+          umma_ts_lo(leader, tmem_base + C::o_col(t), tmem_base + C::s_col(t) + 8 * k, va + (2048 >> 4) * k, C::kIdescO,
+                     (acc || k > 0) ? 1u : 0u);
       };
-      auto wait = [&](uint32_t bar, uint32_t par) { return mbar_wait(bar, par, p.status, kWhereKv8Mma); };
+      auto wait = [&](uint32_t bar, uint32_t par) { return warp_wait(bar, par, p.status, kWhereKv8Mma); };
       auto kv_wait = [&](int L) { return wait(bar_kv_full + 8 * (L % kSlots), (L / kSlots) & 1); };
       bool ok = wait(bar_q, 0) && kv_wait(0);
       if (ok) {
         tc_fence_after();
         issue_s(0, 0);
-        umma_commit(bar_s_full);
+        umma_commit_if(leader, bar_s_full);
         if (two) {
           issue_s(1, 0);
-          umma_commit(bar_s_full + 8);
+          umma_commit_if(leader, bar_s_full + 8);
         }
-        umma_commit(bar_kv_empty);
+        umma_commit_if(leader, bar_kv_empty);
       }
       for (int j = 0; j < n_vis && ok; ++j) {
         const int LV = 2 * j + 1, LK = 2 * j + 2;
@@ -190,7 +200,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (!kv_wait(LK)) break;
           tc_fence_after();
           issue_s(0, LK % kSlots);
-          umma_commit(bar_s_full);
+          umma_commit_if(leader, bar_s_full);
         }
         if (two) {
           if (!wait(bar_p_half + 8, par)) break;
@@ -200,75 +210,81 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tc_fence_after();
           issue_pv(1, LV % kSlots, true, 1);
         }
-        umma_commit(bar_kv_empty + 8 * (LV % kSlots));
+        umma_commit_if(leader, bar_kv_empty + 8 * (LV % kSlots));
         if (has_next) {
           if (two) {
             issue_s(1, LK % kSlots);
-            umma_commit(bar_s_full + 8);
+            umma_commit_if(leader, bar_s_full + 8);
           }
-          umma_commit(bar_kv_empty + 8 * (LK % kSlots));
+          umma_commit_if(leader, bar_kv_empty + 8 * (LK % kSlots));
         }
       }
-      umma_commit(bar_o_done);
-      mbar_wait(bar_o_done, 0, p.status, kWhereKv8Drain);
+      umma_commit_if(leader, bar_o_done);
+      warp_wait(bar_o_done, 0, p.status, kWhereKv8Drain);
     }
     __syncwarp();
-  } else if (warp < 8) {
-    setmaxnreg_dec<kRegsConv>();
+    } else {
     // ---------------------------------------------------------- widening
-    constexpr int kUnits = HD / 16;          // 16-byte pieces of a cached row
-    constexpr int kStep = 128 / kUnits;      // rows of one load of the warpgroup
-    constexpr int kLoads = kTile / kStep;
-    const int ct = (int)threadIdx.x - 128, u = ct % kUnits, row = ct / kUnits;
-    // two pieces of 8 columns; the second box's threads write them in the other order (bank conflicts)
-    const int swap = u >> 2;
-    const uint8_t* src[2] = {c.k + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD + u * 16,
-                             c.v + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD + u * 16};
-    const float* ksp = c.k_scale + (int64_t)bg * c.n_blocks;
-    const float* vsp = c.v_scale + (int64_t)bg * c.n_blocks;
-    uint4 w[kLoads];
-    auto load = [&](int L) {
-      const uint8_t* base = src[L & 1];
-      const int32_t key0 = (kt0 + (L >> 1)) * kTile + row;
+    // A warp takes 32 pieces of 16 bytes at a time, kRows whole rows; the tile's
+    // row groups go round the seven warps.  Eight neighbouring lanes write two
+    // rows' pieces of one box: their chunks of 16 bytes fall on all banks (four
+    // pieces give every other chunk of a row).
+    constexpr int kRows = HD == 128 ? 4 : 8, kRowGroups = kTile / kRows;
+    constexpr int kLoads = (kRowGroups + kConvWarps - 1) / kConvWarps;
+    const int cw = warp - 1;
+    const int u = HD == 128 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3;
+    const int row = cw * kRows + (HD == 128 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane >> 2);
+    const uint8_t* kb = c.k + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD + u * 16;
+    const uint8_t* vb = c.v + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD + u * 16;
+    uint4 wk[kLoads], wv[kLoads];
+    auto load = [&](uint4 (&w)[kLoads], const uint8_t* base, int32_t kt) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
+        const int r = row + i * kConvWarps * kRows;
         w[i] = make_uint4(0, 0, 0, 0);
-        if (key0 + i * kStep < kend) w[i] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)(key0 + i * kStep) * c.ld));
+        if (r < kTile && kt * kTile + r < kend) w[i] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)(kt * kTile + r) * c.ld));
       }
     };
-    if (n_vis > 0) load(0);
-    for (int L = 0; L < 2 * n_vis; ++L) {
-      const int slot = L % kSlots;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar_kv_empty + 8 * slot, ((L / kSlots) & 1) ^ 1, p.status, kWhereKv8Widen)))
-        break;
+    auto widen = [&](const uint4 (&w)[kLoads], int slot) {
       const uint32_t dst = sKV + slot * C::kTileBytes;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int r = row + i * kStep;
-        const uint32_t a0 = cvt_lo(w[i].x), a1 = cvt_hi(w[i].x), a2 = cvt_lo(w[i].y), a3 = cvt_hi(w[i].y);
-        const uint32_t b0 = cvt_lo(w[i].z), b1 = cvt_hi(w[i].z), b2 = cvt_lo(w[i].w), b3 = cvt_hi(w[i].w);
-        const uint32_t da = dst + sw_offset(r, 2 * u), db = dst + sw_offset(r, 2 * u + 1);
-        if (swap) {
-          st_shared16(db, b0, b1, b2, b3);
-          st_shared16(da, a0, a1, a2, a3);
-        } else {
-          st_shared16(da, a0, a1, a2, a3);
-          st_shared16(db, b0, b1, b2, b3);
-        }
+        const int r = row + i * kConvWarps * kRows;
+        if (r >= kTile) break;
+        st_shared16(dst + sw_offset(r, 2 * u), cvt_lo(w[i].x), cvt_hi(w[i].x), cvt_lo(w[i].y), cvt_hi(w[i].y));
+        st_shared16(dst + sw_offset(r, 2 * u + 1), cvt_lo(w[i].z), cvt_hi(w[i].z), cvt_lo(w[i].w), cvt_hi(w[i].w));
       }
-      if (!(L & 1) && ct < 8) {  // the key tile's scales, with its keys
-        const int32_t kt = kt0 + (L >> 1), key = kt * kTile + ct * 16;
-        float4 s = make_float4(1.f, 0.f, 0.f, 0.f);  // a group behind the end: finite, and every key masked
-        if (key < kend) {
-          s.x = __ldg(ksp + key / c.block);
-          scale_log2_parts(__ldg(vsp + key / c.block), s.y, s.z);
-        }
-        scales[((L >> 1) & 3) * 8 + ct] = s;
-      }
+    };
+    auto empty = [&](int L) {
+      return warp_wait(bar_kv_empty + 8 * (L % kSlots), ((L / kSlots) & 1) ^ 1, p.status, kWhereKv8Widen);
+    };
+    auto full = [&](int L) {
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_kv_full + 8 * slot);
-      if (L + 1 < 2 * n_vis) load(L + 1);
+      if (lane == 0) mbar_arrive(bar_kv_full + 8 * (L % kSlots));
+    };
+    if (n_vis > 0) {
+      load(wk, kb, kt0);
+      load(wv, vb, kt0);
+    }
+    for (int j = 0; j < n_vis; ++j) {
+      const int32_t kt = kt0 + j;
+      float4 sc = make_float4(1.f, 0.f, 0.f, 0.f);  // a group behind the end: finite, and every key masked
+      if (cw == 0 && lane < NG && kt * kTile + lane * kGroupKeys < kend) {
+        const int64_t at = (int64_t)bg * c.n_blocks + kt * NG + lane;
+        sc.x = __ldg(c.k_scale + at);
+        scale_log2_parts(__ldg(c.v_scale + at), sc.y, sc.z);
+      }
+      if (!empty(2 * j)) break;
+      widen(wk, (2 * j) % kSlots);
+      if (cw == 0 && lane < NG) scales[(j & 3) * NG + lane] = sc;
+      full(2 * j);
+      if (j + 1 < n_vis) load(wk, kb, kt + 1);
+      if (!empty(2 * j + 1)) break;
+      widen(wv, (2 * j + 1) % kSlots);
+      full(2 * j + 1);
+      if (j + 1 < n_vis) load(wv, vb, kt + 1);
+    }
     }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
@@ -322,8 +338,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_q);
 
-    const uint32_t s_addr = tmem_base + ((uint32_t)lane_base << 16) + s_col[t];
-    const uint32_t o_addr = tmem_base + ((uint32_t)lane_base << 16) + o_col[t];
+    const uint32_t s_addr = tmem_base + ((uint32_t)lane_base << 16) + C::s_col(t);
+    const uint32_t o_addr = tmem_base + ((uint32_t)lane_base << 16) + C::o_col(t);
     const int32_t lim = valid ? row_limit(p, r, len) : kend;  // padding rows see all: they never force the masks
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -332,7 +348,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int j = 0; j < n_vis; ++j) {
         const int32_t kbase = (kt0 + j) * kTile;
         // warp-uniform decisions only: every tcgen05.ld/st below is .sync.aligned
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_s_full + 8 * t, j & 1, p.status, kWhereKv8Softmax))) {
+        if (!warp_wait(bar_s_full + 8 * t, j & 1, p.status, kWhereKv8Softmax)) {
           ok = false;
           break;
         }
@@ -342,7 +358,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
         tmem_ld32(s_addr + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
         tmem_ld32(s_addr + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
-        const float4* sc = scales + (j & 3) * 8;
+        const float4* sc = scales + (j & 3) * NG;
         tmem_ld_wait();
         if (kbase + kTile > lim) {
 #pragma unroll
@@ -351,15 +367,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         float m_new = m;
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          float a = __uint_as_float(s[16 * g]), d = __uint_as_float(s[16 * g + 1]);
+        for (int g = 0; g < NG; ++g) {
+          constexpr int kChains = NG == 1 ? 4 : 2;  // independent three-input chains
+          float mx[kChains];
 #pragma unroll
-          for (int e = 2; e < 16; e += 4) {
-            a = fmax3(a, __uint_as_float(s[16 * g + e]), __uint_as_float(s[16 * g + e + 1]));
-            if (e + 2 < 16) d = fmax3(d, __uint_as_float(s[16 * g + e + 2]), __uint_as_float(s[16 * g + e + 3]));
-          }
+          for (int q = 0; q < kChains; ++q) mx[q] = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < kGroupKeys; e += 2 * kChains)
+#pragma unroll
+            for (int q = 0; q < kChains; ++q)
+              mx[q] = fmax3(mx[q], __uint_as_float(s[kGroupKeys * g + e + 2 * q]), __uint_as_float(s[kGroupKeys * g + e + 2 * q + 1]));
+          float x = fmaxf(mx[0], mx[1]);
+          if constexpr (kChains == 4) x = fmaxf(x, fmaxf(mx[2], mx[3]));
           const float4 k = sc[g];
-          m_new = fmaxf(m_new, fmaf(fmaxf(a, d), fac * k.x, k.y));
+          m_new = fmaxf(m_new, fmaf(x, fac * k.x, k.y));
         }
         const bool first = m == -INFINITY;
         const bool need = !first && m_new > m + kFollow;
@@ -385,20 +406,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         const float mu = m == -INFINITY ? 0.f : m - kTileBias;
 #pragma unroll
-        for (int g2 = 0; g2 < 4; ++g2) {
+        for (int g2 = 0; g2 < 4; ++g2) {  // 32 keys
           uint32_t pk[16];
+          constexpr int kRun = kGroupKeys < 32 ? kGroupKeys : 32;  // keys of one scale
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float4 k = sc[2 * g2 + g];
+          for (int g = 0; g < 32 / kRun; ++g) {
+            const float4 k = sc[(32 * g2 + kRun * g) / kGroupKeys];
             const float f = fac * k.x, off = k.y - mu;
             float rs0 = 0.f, rs1 = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float p0 = ex2_approx(fmaf(__uint_as_float(s[32 * g2 + 16 * g + 2 * e]), f, off));
-              const float p1 = ex2_approx(fmaf(__uint_as_float(s[32 * g2 + 16 * g + 2 * e + 1]), f, off));
+            for (int e = 0; e < kRun / 2; ++e) {
+              const float p0 = ex2_approx(fmaf(__uint_as_float(s[32 * g2 + kRun * g + 2 * e]), f, off));
+              const float p1 = ex2_approx(fmaf(__uint_as_float(s[32 * g2 + kRun * g + 2 * e + 1]), f, off));
               rs0 += p0;
               rs1 += p1;
-              pk[8 * g + e] = pack_f16x2(p0, p1);
+              pk[kRun / 2 * g + e] = pack_f16x2(p0, p1);
             }
             l = fmaf(rs0 + rs1, k.z, l);
           }
@@ -419,7 +441,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const float ref = m - kTileBias;  // o = sum 2^(x - ref) v8, l = sum 2^(x - ref) / vs
     if (t == 0 || two) {
       if (n_vis > 0) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar_o_done, 0, p.status, kWhereKv8Softmax));
+        ok = ok && warp_wait(bar_o_done, 0, p.status, kWhereKv8Softmax);
         tc_fence_after();
       }
       const bool store = valid && dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store);
@@ -634,29 +656,29 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && n_i > 0) {
+    if (n_i > 0) {
+      const uint32_t leader = elect_one();
       bool ok = true;
       for (int i = 0; i < n_i && ok; ++i) {
         const int slot = i % kSlots;
-        ok = mbar_wait(bar_q_full + 8 * slot, (i / kSlots) & 1, p.status, kWhereKv8Mma);
+        ok = warp_wait(bar_q_full + 8 * slot, (i / kSlots) & 1, p.status, kWhereKv8Mma);
         for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
           const int buf = 2 * (i & 1) + t;
-          ok = mbar_wait(bar_s_empty + 8 * buf, ((i >> 1) & 1) ^ 1, p.status, kWhereKv8Mma);
+          ok = warp_wait(bar_s_empty + 8 * buf, ((i >> 1) & 1) ^ 1, p.status, kWhereKv8Mma);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t qa = sQ + slot * C::kTileBytes, ka = sK + t * C::kTileBytes;
+          const uint32_t qa = sw128_desc_lo(sQ + slot * C::kTileBytes, 16), ka = sw128_desc_lo(sK + t * C::kTileBytes, 16);
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k) {
-            const uint32_t off = (k >> 2) * kBoxBytes + (k & 3) * 32;
-            umma_ss(tmem_base + 128u * buf, sw128_desc(qa + off, 16, 1024), sw128_desc(ka + off, 16, 1024), C::kIdesc,
-                    k > 0 ? 1u : 0u);
+            const uint32_t off = ((k >> 2) * kBoxBytes + (k & 3) * 32) >> 4;
+            umma_ss_lo(leader, tmem_base + 128u * buf, qa + off, ka + off, C::kIdesc, k > 0 ? 1u : 0u);
           }
-          umma_commit(bar_s_full + 8 * buf);
+          umma_commit_if(leader, bar_s_full + 8 * buf);
         }
-        if (ok) umma_commit(bar_q_empty + 8 * slot);
+        if (ok) umma_commit_if(leader, bar_q_empty + 8 * slot);
       }
-      umma_commit(bar_done);
-      mbar_wait(bar_done, 0, p.status, kWhereKv8Drain);
+      umma_commit_if(leader, bar_done);
+      warp_wait(bar_done, 0, p.status, kWhereKv8Drain);
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -691,9 +713,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         }
         const bool masked = kbase + kTile > lim;
         const bool any = __any_sync(0xffffffffu, lim > kbase);
-        const bool ok =
-            __all_sync(0xffffffffu, mbar_wait(bar_s_full + 8 * wg, (i >> 1) & 1, p.status, kWhereKv8Softmax));
-        if (!ok) break;
+        if (!warp_wait(bar_s_full + 8 * wg, (i >> 1) & 1, p.status, kWhereKv8Softmax)) break;
         tc_fence_after();
         if (!any) {
           __syncwarp();
@@ -830,15 +850,23 @@ cosmot_status prepare(K kern, int smem, int64_t regs, int threads, uint64_t& don
   return COSMOT_OK;
 }
 
-template <int HD>
-cosmot_status launch_attention(const Cache& c, const Query& p, const TilePlan& t, cudaStream_t s) {
+template <int HD, int NG>
+cosmot_status launch_tiles(const Cache& c, const Query& p, const TilePlan& t, cudaStream_t s) {
   static uint64_t done = 0;
-  cosmot_status st = prepare(tile_attention_kernel<HD>, AttnCfg<HD>::kSmem,
-                             128 * (kRegsMma + kRegsConv) + 256 * kRegsSoftmax, kAttnThreads, done);
+  const cosmot_status st = prepare(tile_attention_kernel<HD, NG>, AttnCfg<HD>::kSmem, 256 * (kRegsIo + kRegsSoftmax),
+                                   kAttnThreads, done);
   if (st != COSMOT_OK) return st;
   const int64_t grid = t.n_full + (int64_t)t.n_tail * t.splits;
-  st = launch_status(launch_pdl(tile_attention_kernel<HD>, dim3((unsigned)grid), dim3(kAttnThreads), AttnCfg<HD>::kSmem, s,
-                                nullptr, c, p, t));
+  return launch_status(launch_pdl(tile_attention_kernel<HD, NG>, dim3((unsigned)grid), dim3(kAttnThreads),
+                                  AttnCfg<HD>::kSmem, s, nullptr, c, p, t));
+}
+
+template <int HD>
+cosmot_status launch_attention(const Cache& c, const Query& p, const TilePlan& t, cudaStream_t s) {
+  const cosmot_status st = c.block == 128  ? launch_tiles<HD, 1>(c, p, t, s)
+                           : c.block == 64 ? launch_tiles<HD, 2>(c, p, t, s)
+                           : c.block == 32 ? launch_tiles<HD, 4>(c, p, t, s)
+                                           : launch_tiles<HD, 8>(c, p, t, s);
   if (st != COSMOT_OK || t.n_tail == 0) return st;
   const int64_t units = (int64_t)t.n_tail * 2 * kTile * (HD / 8);
   return launch_status(launch_pdl(tile_join_kernel<HD>, dim3((unsigned)((units + 255) / 256)), dim3(256), 0, s, nullptr, c,
