@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   float4* scales = reinterpret_cast<float4*>(smem + (2 + kSlots) * C::kTileBytes + 256);
   constexpr int kGroupKeys = kTile / NG;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
   // work item: the pairs of all heads in turn (causal: the longest first)
   int32_t item = (int32_t)blockIdx.x, split = 0, splits = 1;
   if (item >= plan.n_full) {
@@ -145,11 +145,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int32_t kend = row_limit(p, r_end - 1, len);
   const int32_t n_kt = (kend + kTile - 1) / kTile;
   const int32_t kt0 = (int32_t)((int64_t)split * n_kt / splits), kt1 = (int32_t)((int64_t)(split + 1) * n_kt / splits);
-  const int32_t n_vis = kt1 - kt0;  // key tiles of this CTA
+  const int32_t n_vis = __shfl_sync(0xffffffffu, kt1 - kt0, 0);  // key tiles of this CTA
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
 
   if (warp < 8) {
     setmaxnreg_dec<kRegsIo>();
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   float* sums = reinterpret_cast<float*>(smem + (2 + kSlots) * C::kTileBytes + 256);  // [4 warpgroups][4 warps][8 groups]
   float* parts = sums + 4 * 4 * 8;                                                    // [cluster][16 groups]
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
   const uint32_t rank = cluster_ctarank(), ranks = gridDim.z;
   const int32_t bg = blockIdx.y, b = bg / c.n_kv, kvh = bg % c.n_kv;
   const int32_t k0 = (int32_t)blockIdx.x * 2 * kTile;
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   }
   const int32_t i0 = i_first + (int32_t)((int64_t)(n_all - i_first) * rank / ranks);
   const int32_t i1 = i_first + (int32_t)((int64_t)(n_all - i_first) * (rank + 1) / ranks);
-  const int32_t n_i = i1 - i0;
+  const int32_t n_i = __shfl_sync(0xffffffffu, i1 - i0, 0);
 
   if (n_i > 0 && warp >= 4) {
     // the keys, widened to bf16 (exact), rows behind the end zero; the rows of a query tile that TMA never writes, zero
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   else
     __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
 
   if (warp == 0) {
     if (lane == 0 && n_i > 0) {
