@@ -26,7 +26,7 @@
 // (bf16), and every thread of four warpgroups owns one query row of a tile:
 // per group of 16 keys it adds 2^(s f - lse).  Nothing but the sums leaves the
 // CTA; a cluster may share the queries of one key range, and the sums are
-// joined in a fixed order.
+// joined in a fixed order.  A quarter of the exponentials runs on the FMA pipe.
 #include "kv8.cuh"
 
 #include <mutex>
@@ -528,13 +528,22 @@ __global__ void __launch_bounds__(256) tile_join_kernel(const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ weighing
-constexpr int kWeighThreads = 640;  // warps 0-3: TMA, MMA; four warpgroups of rows
-constexpr int kWeighMaxCluster = 8;
+// Warp 0 loads the queries' tiles (TMA), warp 1 issues the products, warps 2-3
+// widen the next item's keys, four warpgroups own the rows of two query tiles
+// x two key tiles.  Items (256 keys of a sequence and key head) go round the
+// CTAs; nothing drains between two items.
+constexpr int kWeighThreads = 640;
+constexpr int kWeighMaxCluster = 4;
+constexpr int kQSlots = 3;
+constexpr int kPolyPairs = 2;  // of 8 pairs of exponentials, those on the FMA pipe
 
 template <int HD>
 struct WeighCfg {
   static constexpr int kTileBytes = kTile * HD * 2;
-  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 256 + 4 * 4 * 8 * 4 + kWeighMaxCluster * 16 * 4 + 1024;
+  static constexpr int kBars = (4 + kQSlots) * kTileBytes;  // two buffers of two key tiles, the queries' ring
+  static constexpr int kSums = kBars + 192;                 // [2][4 warpgroups][4 warps][8 groups]
+  static constexpr int kParts = kSums + 2 * 4 * 4 * 8 * 4;  // [2][cluster][16 groups]
+  static constexpr int kSmem = kParts + 2 * kWeighMaxCluster * 16 * 4 + 1024;
   static constexpr uint32_t kIdesc = idesc_bf16_f32(kTile, kTile, false, false);
 };
 
@@ -547,32 +556,96 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// q_tile: queries of a tile (kTile / group), its rows q_tile * group <= 128.
+constexpr float kExp2C1 = 6.931470037e-01f, kExp2C2 = 2.402224243e-01f, kExp2C3 = 5.550733581e-02f, kExp2C4 = 9.671512991e-03f, kExp2C5 = 1.326472731e-03f;
+
+// Into [-127, 128], NaN kept.
+__device__ __forceinline__ float clamp_exp2(float x) {
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;\n\tmin.NaN.f32 %0, %0, 0f43000000;" : "+f"(x));
+  return x;
+}
+
+// 2^x of a pair on the FMA pipe: n = round(x), 2^n by its exponent bits (zero
+// at -127, infinity at 128), 2^(x - n) by a polynomial of degree 5
+// with constant 1, fitted here for the least relative error on [-1/2, 1/2]
+// (1.9e-7 of the value, float32 arithmetic included).
+__device__ __forceinline__ void exp2_fma(uint64_t x, float& y0, float& y1) {
+  float a, b;
+  unpack_f32x2(x, a, b);
+  x = pack_f32x2(clamp_exp2(a), clamp_exp2(b));
+  const uint64_t magic = pack_f32x2(12582912.f, 12582912.f);  // 1.5 * 2^23: the sum's low bits are round(x)
+  const uint64_t t = add_f32x2(x, magic);
+  const uint64_t f = add_f32x2(x, neg_f32x2(add_f32x2(t, neg_f32x2(magic))));
+  uint64_t r = pack_f32x2(kExp2C5, kExp2C5);
+  r = fma_f32x2(r, f, pack_f32x2(kExp2C4, kExp2C4));
+  r = fma_f32x2(r, f, pack_f32x2(kExp2C3, kExp2C3));
+  r = fma_f32x2(r, f, pack_f32x2(kExp2C2, kExp2C2));
+  r = fma_f32x2(r, f, pack_f32x2(kExp2C1, kExp2C1));
+  r = fma_f32x2(r, f, pack_f32x2(1.f, 1.f));
+  float t0, t1, r0, r1;
+  unpack_f32x2(t, t0, t1);
+  unpack_f32x2(r, r0, r1);
+  y0 = r0 * __int_as_float((__float_as_int(t0) << 23) + 0x3f800000);
+  y1 = r1 * __int_as_float((__float_as_int(t1) << 23) + 0x3f800000);
+}
+
+struct WeighItem {
+  int32_t bg, b, k0, k_end, len, i0, n_i;  // keys [k0, k_end), query tiles [i0, i0 + n_i) of this CTA; k_end = k0: none
+  bool two;
+};
+
+__device__ __forceinline__ WeighItem weigh_item(const Cache& c, const Query& p, int64_t item, int32_t q_tile, int32_t rank,
+                                                int32_t ranks) {
+  WeighItem w;
+  const int32_t heads = c.batch * c.n_kv;  // one key range of every head, then the next
+  w.bg = (int32_t)(item % heads);
+  w.b = w.bg / c.n_kv;
+  w.k0 = (int32_t)(item / heads) * 2 * kTile;
+  w.len = __shfl_sync(0xffffffffu, shown_rows(c, w.b, p.n_new, p.status, threadIdx.x == 0 && rank == 0), 0);
+  w.k_end = min(w.len, w.k0 + 2 * kTile);
+  if (w.k0 >= w.len) w.k_end = w.k0;
+  w.two = w.k0 + kTile < w.k_end;
+  // query tiles that see a key of the range (causal: the last ones), shared by the cluster
+  const int32_t n_all = (int32_t)((p.n_q + q_tile - 1) / q_tile);
+  int32_t first = w.k_end > w.k0 ? 0 : n_all;
+  if (p.causal && w.k_end > w.k0) {  // query i sees keys <= len - n_q + i
+    const int64_t q_first = (int64_t)w.k0 - (w.len - p.n_q);
+    if (q_first > 0) first = (int32_t)(q_first / q_tile);  // < n_all as k0 < len
+  }
+  w.i0 = first + (int32_t)((int64_t)(n_all - first) * rank / ranks);
+  w.n_i = first + (int32_t)((int64_t)(n_all - first) * (rank + 1) / ranks) - w.i0;
+  return w;
+}
+
+// q_tile: queries of a tile (kTile / group), its rows q_tile * group <= 128;
+// ranges: key ranges of 256 in the capacity.
 template <int HD>
 __global__ void __launch_bounds__(kWeighThreads, 1)
     tile_weigh_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ Cache c,
-                      const __grid_constant__ Query p, float decay, float* __restrict__ weight, int32_t q_tile) {
+                      const __grid_constant__ Query p, float decay, float* __restrict__ weight, int32_t q_tile,
+                      int32_t ranges) {
   using C = WeighCfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sK = smem_u32(smem);
-  const uint32_t sQ = sK + 2 * C::kTileBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (2 + kSlots) * C::kTileBytes);
-  const uint32_t bar_q_full = smem_u32(bars);              // [kSlots]
-  const uint32_t bar_q_empty = bar_q_full + 8 * kSlots;    // [kSlots]
-  const uint32_t bar_s_full = bar_q_empty + 8 * kSlots;    // [4]
+  const uint32_t sQ = sK + 4 * C::kTileBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
+  const uint32_t bar_q_full = smem_u32(bars);              // [kQSlots]
+  const uint32_t bar_q_empty = bar_q_full + 8 * kQSlots;   // [kQSlots]
+  const uint32_t bar_s_full = bar_q_empty + 8 * kQSlots;   // [4]
   const uint32_t bar_s_empty = bar_s_full + 32;            // [4]
-  const uint32_t bar_done = bar_s_empty + 32;              // [1]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kSlots + 9);
-  float* sums = reinterpret_cast<float*>(smem + (2 + kSlots) * C::kTileBytes + 256);  // [4 warpgroups][4 warps][8 groups]
-  float* parts = sums + 4 * 4 * 8;                                                    // [cluster][16 groups]
+  const uint32_t bar_k_full = bar_s_empty + 32;            // [2]
+  const uint32_t bar_k_empty = bar_k_full + 16;            // [2]
+  const uint32_t bar_done = bar_k_empty + 16;              // [1]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kQSlots + 13);
+  float* sums = reinterpret_cast<float*>(smem + C::kSums);
+  float* parts = reinterpret_cast<float*>(smem + C::kParts);
 
-  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
-  const uint32_t rank = cluster_ctarank(), ranks = gridDim.z;
-  const int32_t bg = blockIdx.y, b = bg / c.n_kv, kvh = bg % c.n_kv;
-  const int32_t k0 = (int32_t)blockIdx.x * 2 * kTile;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int32_t ranks = gridDim.y, rank = blockIdx.y;  // the cluster runs along y
+  const int64_t items = (int64_t)c.batch * c.n_kv * ranges;
+  const int32_t tile_rows = q_tile * p.group;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kSlots; ++s) {
+    for (int s = 0; s < kQSlots; ++s) {
       mbar_init(bar_q_full + 8 * s, 1);
       mbar_init(bar_q_empty + 8 * s, 1);
     }
@@ -580,240 +653,291 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       mbar_init(bar_s_full + 8 * s, 1);
       mbar_init(bar_s_empty + 8 * s, 4);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar_k_full + 8 * s, 2);
+      mbar_init(bar_k_empty + 8 * s, 1);
+    }
     mbar_init(bar_done, 1);
     fence_barrier_init();
   }
-  pdl_trigger();
-  pdl_wait();
-  const int32_t len = shown_rows(c, b, p.n_new, p.status, threadIdx.x == 0 && rank == 0);
-  if (k0 >= len) return;  // the whole cluster
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  const int32_t k_end = k0 + 2 * kTile < len ? k0 + 2 * kTile : len;
-  const bool two = k0 + kTile < k_end;
-  const int32_t tile_rows = q_tile * p.group;
-  // query tiles of this CTA: those that see a key of its range (causal: the last ones), shared by the cluster
-  const int32_t n_all = (int32_t)((p.n_q + q_tile - 1) / q_tile);
-  int32_t i_first = 0;
-  if (p.causal) {  // query i sees keys <= len - n_q + i
-    const int64_t q_first = (int64_t)k0 - (len - p.n_q);
-    if (q_first > 0) i_first = (int32_t)(q_first / q_tile);  // < n_all as k0 < len
-  }
-  const int32_t i0 = i_first + (int32_t)((int64_t)(n_all - i_first) * rank / ranks);
-  const int32_t i1 = i_first + (int32_t)((int64_t)(n_all - i_first) * (rank + 1) / ranks);
-  const int32_t n_i = __shfl_sync(0xffffffffu, i1 - i0, 0);
-
-  if (n_i > 0 && warp >= 4) {
-    // the keys, widened to bf16 (exact), rows behind the end zero; the rows of a query tile that TMA never writes, zero
-    constexpr int kUnits = HD / 16, kStep = 512 / kUnits;
-    const int ct = (int)threadIdx.x - 128, u = ct % kUnits;
-    const uint8_t* src = c.k + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD + u * 16;
-#pragma unroll
-    for (int i = 0; i < 2 * kTile / kStep; ++i) {
-      const int row = ct / kUnits + i * kStep;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (k0 + row < k_end) w = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(k0 + row) * c.ld));
-      const uint32_t* x = reinterpret_cast<const uint32_t*>(&w);
-      uint32_t y[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = cvt_lo(x[e]), hi = cvt_hi(x[e]);
-        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-        y[2 * e] = pack_bf16x2(f0.x, f0.y);
-        y[2 * e + 1] = pack_bf16x2(f1.x, f1.y);
-      }
-      const uint32_t dst = sK + (row >> 7) * C::kTileBytes;
-      st_shared16(dst + sw_offset(row & 127, 2 * u), y[0], y[1], y[2], y[3]);
-      st_shared16(dst + sw_offset(row & 127, 2 * u + 1), y[4], y[5], y[6], y[7]);
-    }
+  if (warp >= 4 && tile_rows < kTile) {  // the rows of a query tile that TMA never writes
     const int pieces = (kTile - tile_rows) * (HD / 8);
-    for (int i = ct; i < kSlots * pieces; i += 512) {
+    for (int i = (int)threadIdx.x - 128; i < kQSlots * pieces; i += 512) {
       const int q = i % pieces;
       st_shared16(sQ + (i / pieces) * C::kTileBytes + sw_offset(tile_rows + q / (HD / 8), q % (HD / 8)), 0, 0, 0, 0);
     }
     fence_proxy_async_smem();
   }
+  pdl_trigger();
+  pdl_wait();
   tc_fence_before();
   if (ranks > 1)
-    cluster_sync();  // the first CTA of the cluster has started before anything is written to it
+    cluster_sync();  // every CTA of the cluster has started before anything is written to it
   else
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
 
   if (warp == 0) {
-    if (lane == 0 && n_i > 0) {
-      tma_prefetch_desc(&tmap_q);
-      int armed = 0;
-      for (int i = 0; i < n_i; ++i) {
-        const int slot = i % kSlots;
-        if (!mbar_wait(bar_q_empty + 8 * slot, ((i / kSlots) & 1) ^ 1, p.status, kWhereKv8Widen)) break;
-        mbar_arrive_expect_tx(bar_q_full + 8 * slot, (uint32_t)tile_rows * HD * 2);
-        for (int bx = 0; bx < HD / 64; ++bx)
-          tma_load_4d(sQ + slot * C::kTileBytes + bx * kBoxBytes, &tmap_q, bar_q_full + 8 * slot, bx * 64,
-                      kvh * p.group, (i0 + i) * q_tile, b);
-        armed = i + 1;
-      }
-      // every copy lands before the CTA may exit
-      for (int i = armed > kSlots ? armed - kSlots : 0; i < armed; ++i) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(bar_q_full + 8 * (i % kSlots), (i / kSlots) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {
+    tma_prefetch_desc(&tmap_q);
+    int n = 0;  // tiles so far
+    bool ok = true;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+      const WeighItem w = weigh_item(c, p, item, q_tile, rank, ranks);
+      for (int i = 0; i < w.n_i && ok; ++i, ++n) {
+        const int slot = n % kQSlots;
+        ok = warp_wait(bar_q_empty + 8 * slot, ((n / kQSlots) & 1) ^ 1, p.status, kWhereKv8Widen);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar_q_full + 8 * slot, (uint32_t)tile_rows * HD * 2);
+          for (int bx = 0; bx < HD / 64; ++bx)
+            tma_load_4d(sQ + slot * C::kTileBytes + bx * kBoxBytes, &tmap_q, bar_q_full + 8 * slot, bx * 64,
+                        (w.bg % c.n_kv) * p.group, (w.i0 + i) * q_tile, w.b);
         }
+        __syncwarp();
+      }
+      if (ranks > 1) cluster_sync();
+    }
+    // every copy lands before the CTA may exit
+    for (int i = n > kQSlots ? n - kQSlots : 0; i < n; ++i) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(bar_q_full + 8 * (i % kQSlots), (i / kQSlots) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (n_i > 0) {
-      const uint32_t leader = elect_one();
-      bool ok = true;
-      for (int i = 0; i < n_i && ok; ++i) {
-        const int slot = i % kSlots;
-        ok = warp_wait(bar_q_full + 8 * slot, (i / kSlots) & 1, p.status, kWhereKv8Mma);
-        for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
-          const int buf = 2 * (i & 1) + t;
-          ok = warp_wait(bar_s_empty + 8 * buf, ((i >> 1) & 1) ^ 1, p.status, kWhereKv8Mma);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t qa = sw128_desc_lo(sQ + slot * C::kTileBytes, 16), ka = sw128_desc_lo(sK + t * C::kTileBytes, 16);
+    const uint32_t leader = elect_one();
+    int n = 0, used[2][2] = {{0, 0}, {0, 0}}, done = 0;  // query tiles; uses of S buffer [phase][key tile]; items
+    bool ok = true;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+      const WeighItem w = weigh_item(c, p, item, q_tile, rank, ranks);
+      if (w.n_i > 0 && ok) {
+        const int kbuf = done & 1;
+        ok = warp_wait(bar_k_full + 8 * kbuf, (done >> 1) & 1, p.status, kWhereKv8Mma);
+        for (int i = 0; i < w.n_i && ok; ++i, ++n) {
+          const int slot = n % kQSlots, phase = n & 1;
+          ok = warp_wait(bar_q_full + 8 * slot, (n / kQSlots) & 1, p.status, kWhereKv8Mma);
 #pragma unroll
-          for (int k = 0; k < HD / 16; ++k) {
-            const uint32_t off = ((k >> 2) * kBoxBytes + (k & 3) * 32) >> 4;
-            umma_ss_lo(leader, tmem_base + 128u * buf, qa + off, ka + off, C::kIdesc, k > 0 ? 1u : 0u);
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || (t == 1 && !w.two)) break;
+            const int buf = 2 * phase + t, u = phase ? used[1][t]++ : used[0][t]++;
+            ok = warp_wait(bar_s_empty + 8 * buf, (u & 1) ^ 1, p.status, kWhereKv8Mma);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t qa = sw128_desc_lo(sQ + slot * C::kTileBytes, 16);
+            const uint32_t ka = sw128_desc_lo(sK + (2 * kbuf + t) * C::kTileBytes, 16);
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k) {
+              const uint32_t off = ((k >> 2) * kBoxBytes + (k & 3) * 32) >> 4;
+              umma_ss_lo(leader, tmem_base + 128u * buf, qa + off, ka + off, C::kIdesc, k > 0 ? 1u : 0u);
+            }
+            umma_commit_if(leader, bar_s_full + 8 * buf);
           }
-          umma_commit_if(leader, bar_s_full + 8 * buf);
+          if (ok) umma_commit_if(leader, bar_q_empty + 8 * slot);
         }
-        if (ok) umma_commit_if(leader, bar_q_empty + 8 * slot);
+        if (ok) umma_commit_if(leader, bar_k_empty + 8 * kbuf);
+        ++done;
       }
-      umma_commit_if(leader, bar_done);
-      warp_wait(bar_done, 0, p.status, kWhereKv8Drain);
+      if (ranks > 1) cluster_sync();
     }
-    __syncwarp();
-  } else if (warp >= 4) {
+    umma_commit_if(leader, bar_done);
+    warp_wait(bar_done, 0, p.status, kWhereKv8Drain);
+  } else if (warp < 4) {
+    // keys to bf16 (exact), rows behind the end zero; the two warps take four (hd 64: eight) rows in turn
+    constexpr int kRows = HD == 128 ? 4 : 8, kAhead = 4;
+    const int u = HD == 128 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3;
+    const int row0 = (warp - 2) * kRows + (HD == 128 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane >> 2);
+    int done = 0;
+    bool ok = true;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+      const WeighItem w = weigh_item(c, p, item, q_tile, rank, ranks);
+      if (w.n_i > 0 && ok) {
+        const uint8_t* src = c.k + (int64_t)w.b * c.bstride * c.ld + (int64_t)(w.bg % c.n_kv) * HD + u * 16;
+        const uint32_t dst = sK + (done & 1) * 2 * C::kTileBytes;
+        ok = warp_wait(bar_k_empty + 8 * (done & 1), ((done >> 1) & 1) ^ 1, p.status, kWhereKv8Widen);
+        const int rows = w.two ? 2 * kTile : kTile;
+        for (int r0 = row0; r0 < rows && ok; r0 += 2 * kRows * kAhead) {
+          uint4 x[kAhead];
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const int row = r0 + 2 * kRows * i;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (w.k0 + row < w.k_end) x[i] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(w.k0 + row) * c.ld));
+          }
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const int row = r0 + 2 * kRows * i;
+            const uint32_t* z = reinterpret_cast<const uint32_t*>(&x[i]);
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t lo = cvt_lo(z[e]), hi = cvt_hi(z[e]);
+              const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+              const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+              y[2 * e] = pack_bf16x2(f0.x, f0.y);
+              y[2 * e + 1] = pack_bf16x2(f1.x, f1.y);
+            }
+            const uint32_t d = dst + (row >> 7) * C::kTileBytes;
+            st_shared16(d + sw_offset(row & 127, 2 * u), y[0], y[1], y[2], y[3]);
+            st_shared16(d + sw_offset(row & 127, 2 * u + 1), y[4], y[5], y[6], y[7]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bar_k_full + 8 * (done & 1));
+        ++done;
+      }
+      if (ranks > 1) cluster_sync();
+    }
+  } else {
     const int wg = (warp - 4) >> 2, t = wg & 1, phase = wg >> 1;
     const int lane_base = (warp & 3) * 32, row = lane_base + lane;
-    const int32_t kbase = k0 + t * kTile;
-    float acc[8];
-    float f[8];
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      acc[g] = 0.f;
-      const int32_t key = kbase + 16 * g;
-      f[g] = key < k_end ? p.scale_log2 * __ldg(c.k_scale + (int64_t)bg * c.n_blocks + key / c.block) : 0.f;
-    }
     const int32_t qr = row / p.group, hr = row % p.group;  // query and head of this row in a tile
-    const float* lse_row = p.lse + ((int64_t)b * p.n_heads + kvh * p.group + hr) * p.n_q;
     const uint32_t addr = tmem_base + ((uint32_t)lane_base << 16) + 128u * wg;
-    if (t == 0 || two) {
-#pragma unroll 1
-      for (int i = phase; i < n_i; i += 2) {
-        const int64_t qi = (int64_t)(i0 + i) * q_tile + qr;
-        // rows that are not there weigh 2^-inf; rows that saw nothing (lse = -inf) are hidden from every key
-        float ls = INFINITY;
-        int32_t lim = k_end;
-        if (row < tile_rows && qi < p.n_q) {
-          ls = __ldg(lse_row + qi) * kLog2e;
-          if (p.causal) {
-            const int64_t x = (int64_t)len - p.n_q + qi + 1;
-            lim = x < 0 ? 0 : (x < k_end ? (int32_t)x : k_end);
-          }
-          if (ls == -INFINITY) lim = 0;
-        }
-        const bool masked = kbase + kTile > lim;
-        const bool any = __any_sync(0xffffffffu, lim > kbase);
-        if (!warp_wait(bar_s_full + 8 * wg, (i >> 1) & 1, p.status, kWhereKv8Softmax)) break;
-        tc_fence_after();
-        if (!any) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_s_empty + 8 * wg);
-          continue;
-        }
-        uint32_t s[2][32];
-        tmem_ld32(addr, s[0]);
+    int n = 0, used = 0, parity = 0;  // query tiles, uses of this S buffer, sums' buffer
+    bool ok = true;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+      const WeighItem w = weigh_item(c, p, item, q_tile, rank, ranks);
+      if (w.k_end == w.k0) {
+        if (ranks > 1) cluster_sync();
+        continue;
+      }
+      const int32_t kbase = w.k0 + t * kTile;
+      float acc[8], f[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          tmem_ld_wait();
-          if (q < 3) {
-            tmem_ld32(addr + 32 * (q + 1), s[(q + 1) & 1]);
-          } else {  // S is in registers: the next product may overwrite it
-            tc_fence_before();
+      for (int g = 0; g < 8; ++g) {
+        acc[g] = 0.f;
+        const int32_t key = kbase + 16 * g;
+        f[g] = key < w.k_end ? p.scale_log2 * __ldg(c.k_scale + (int64_t)w.bg * c.n_blocks + key / c.block) : 0.f;
+      }
+      const float* lse_row = p.lse + ((int64_t)w.b * p.n_heads + (w.bg % c.n_kv) * p.group + hr) * p.n_q;
+      if (t == 0 || w.two) {
+#pragma unroll 1
+        for (int i = (phase ^ n) & 1; i < w.n_i && ok; i += 2) {
+          const int64_t qi = (int64_t)(w.i0 + i) * q_tile + qr;
+          // rows that are not there weigh 2^-inf; rows that saw nothing (lse = -inf) are hidden from every key
+          float ls = INFINITY;
+          int32_t lim = w.k_end;
+          if (row < tile_rows && qi < p.n_q) {
+            ls = __ldg(lse_row + qi) * kLog2e;
+            if (p.causal) {
+              const int64_t x = (int64_t)w.len - p.n_q + qi + 1;
+              lim = x < 0 ? 0 : (x < w.k_end ? (int32_t)x : w.k_end);
+            }
+            if (ls == -INFINITY) lim = 0;
+          }
+          const bool masked = kbase + kTile > lim;
+          const bool any = __any_sync(0xffffffffu, lim > kbase);
+          ok = warp_wait(bar_s_full + 8 * wg, used & 1, p.status, kWhereKv8Softmax);
+          ++used;
+          if (!ok) break;
+          tc_fence_after();
+          if (!any) {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_s_empty + 8 * wg);
+            continue;
           }
-          uint32_t(&x)[32] = s[q & 1];
-          if (masked) {
+          uint32_t s[2][32];
+          tmem_ld32(addr, s[0]);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float pe = ex2_approx(fmaf(__uint_as_float(x[e]), f[2 * q + (e >> 4)], -ls));
-              acc[2 * q + (e >> 4)] += kbase + 32 * q + e < lim ? pe : 0.f;
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld_wait();
+            if (q < 3) {
+              tmem_ld32(addr + 32 * (q + 1), s[(q + 1) & 1]);
+            } else {  // S is in registers: the next product may overwrite it
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar_s_empty + 8 * wg);
             }
-          } else {
+            uint32_t(&x)[32] = s[q & 1];
+            if (masked) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const uint64_t f2 = pack_f32x2(f[2 * q + g], f[2 * q + g]), ls2 = pack_f32x2(-ls, -ls);
-              uint64_t a = pack_f32x2(0.f, 0.f);
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                float p0, p1;
-                unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[16 * g + e]), __uint_as_float(x[16 * g + e + 1])), f2, ls2),
-                             p0, p1);
-                a = add_f32x2(a, pack_f32x2(ex2_approx(p0), ex2_approx(p1)));
+              for (int e = 0; e < 32; ++e) {
+                const float pe = ex2_approx(fmaf(__uint_as_float(x[e]), f[2 * q + (e >> 4)], -ls));
+                acc[2 * q + (e >> 4)] += kbase + 32 * q + e < lim ? pe : 0.f;
               }
-              float a0, a1;
-              unpack_f32x2(a, a0, a1);
-              acc[2 * q + g] += a0 + a1;
+            } else {
+              const uint64_t ls2 = pack_f32x2(-ls, -ls);
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const uint64_t f2 = pack_f32x2(f[2 * q + g], f[2 * q + g]);
+                float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const uint64_t v = fma_f32x2(
+                      pack_f32x2(__uint_as_float(x[16 * g + 2 * e]), __uint_as_float(x[16 * g + 2 * e + 1])), f2, ls2);
+                  float p0, p1;
+                  if (e % 4 == 1 && e / 4 < kPolyPairs) {
+                    exp2_fma(v, p0, p1);
+                  } else {
+                    unpack_f32x2(v, p0, p1);
+                    p0 = ex2_approx(p0);
+                    p1 = ex2_approx(p1);
+                  }
+                  a0 += p0;
+                  a1 += p1;
+                }
+                acc[2 * q + g] += a0 + a1;
+              }
             }
           }
         }
       }
-    }
+      n += w.n_i;
+      // 16 group sums of this CTA, then of the cluster, each added in a fixed order
+      float* my_sums = sums + parity * 128;
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
+      for (int g = 0; g < 8; ++g) {
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) acc[g] += __shfl_xor_sync(0xffffffffu, acc[g], off);
-      if (lane == g) sums[(wg * 4 + (warp & 3)) * 8 + g] = acc[g];
+        for (int off = 16; off > 0; off >>= 1) acc[g] += __shfl_xor_sync(0xffffffffu, acc[g], off);
+        if (lane == g) my_sums[(wg * 4 + (warp & 3)) * 8 + g] = acc[g];
+      }
+      asm volatile("bar.sync 1, 512;" ::: "memory");  // the four warpgroups of rows
+      float* my_parts = parts + parity * kWeighMaxCluster * 16;
+      if (warp == 4) {
+        const int kt = (lane >> 3) & 1, g = lane & 7;
+        float x = 0.f;
+#pragma unroll
+        for (int ph = 0; ph < 2; ++ph)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x += my_sums[((2 * ph + kt) * 4 + q) * 8 + g];
+        if (lane < 16) {
+          const uint32_t at = smem_u32(my_parts + rank * 16 + lane);
+          if (ranks > 1)
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(at, 0)), "f"(x) : "memory");
+          else
+            my_parts[lane] = x;
+        }
+        __syncwarp();
+      }
+      if (ranks > 1) cluster_sync();
+      if (warp == 4 && rank == 0) {
+        const int n_groups = c.block / 16;  // groups of a block
+        const int32_t key = w.k0 + lane * c.block;
+        if (lane < 16 / n_groups && key < w.k_end) {
+          float x = 0.f;
+          for (int r = 0; r < ranks; ++r)
+            for (int g = 0; g < n_groups; ++g) x += my_parts[r * 16 + lane * n_groups + g];
+          const int32_t blk = key / c.block;
+          if (dcheck(blk < c.n_blocks, p.status, kWhereKv8Store)) {
+            float* out = weight + (int64_t)w.bg * c.n_blocks + blk;
+            *out = fmaf(decay, *out, x);
+          }
+        }
+        __syncwarp();
+      }
+      parity ^= 1;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, 512);
-  // 16 group sums of this CTA, then of the cluster, each added in a fixed order
-  if (threadIdx.x < 16) {
-    const int t = threadIdx.x >> 3, g = threadIdx.x & 7;
-    float x = 0.f;
-#pragma unroll
-    for (int ph = 0; ph < 2; ++ph)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) x += sums[((2 * ph + t) * 4 + w) * 8 + g];
-    if (ranks > 1) {
-      const uint32_t at = mapa_shared(smem_u32(parts + rank * 16 + threadIdx.x), 0);
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
-    } else {
-      parts[threadIdx.x] = x;
-    }
-  }
-  __syncwarp();
-  if (ranks > 1)
-    cluster_sync();
-  else
-    __syncthreads();
-  const int n_groups = c.block / 16;  // groups of a block
-  if (rank == 0 && (int)threadIdx.x < 16 / n_groups) {
-    const int32_t key = k0 + (int32_t)threadIdx.x * c.block;
-    if (key < k_end) {
-      float x = 0.f;
-      for (uint32_t r = 0; r < ranks; ++r)
-        for (int g = 0; g < n_groups; ++g) x += parts[r * 16 + threadIdx.x * n_groups + g];
-      const int32_t blk = key / c.block;
-      if (dcheck(blk < c.n_blocks, p.status, kWhereKv8Store)) {
-        float* w = weight + (int64_t)bg * c.n_blocks + blk;
-        *w = fmaf(decay, *w, x);
-      }
-    }
-  }
+  if (ranks > 1) cluster_sync();  // nothing is written to a CTA that has left
 }
 
 // ------------------------------------------------------------------ host
@@ -899,18 +1023,19 @@ cosmot_status launch_weigh(const Cache& c, const Query& p, float decay, float* w
                          (uint64_t)(c.batch > 1 ? p.q_bstride : p.n_q), 64, (uint32_t)p.group, (uint32_t)q_tile);
   if (st != COSMOT_OK) return st;
   const int64_t heads = (int64_t)c.batch * c.n_kv, n_all = (p.n_q + q_tile - 1) / q_tile;
-  const int64_t live = heads * (((int64_t)max_len + 2 * kTile - 1) / (2 * kTile));
+  const int32_t ranges = (c.capacity + 2 * kTile - 1) / (2 * kTile);
+  const int64_t live = heads * (((int64_t)max_len + 2 * kTile - 1) / (2 * kTile)), items = heads * ranges, sms = num_sms();
   // a key range's queries are shared by a cluster where there are fewer key ranges than SMs
-  unsigned ranks = 1;
-  while (ranks < (unsigned)kWeighMaxCluster && live * ranks * 2 <= num_sms() && n_all >= 4 * ranks) ranks *= 2;
+  int ranks = 1;
+  while (ranks < kWeighMaxCluster && live * ranks * 2 <= sms && n_all >= 4 * ranks) ranks *= 2;
   cudaLaunchAttribute cl{};
   cl.id = cudaLaunchAttributeClusterDimension;
   cl.val.clusterDim.x = 1;
-  cl.val.clusterDim.y = 1;
-  cl.val.clusterDim.z = ranks;
-  const dim3 grid((unsigned)((c.capacity + 2 * kTile - 1) / (2 * kTile)), (unsigned)heads, ranks);
+  cl.val.clusterDim.y = (unsigned)ranks;
+  cl.val.clusterDim.z = 1;
+  const dim3 grid((unsigned)(items < sms / ranks ? items : sms / ranks), (unsigned)ranks);
   return launch_status(launch_pdl(tile_weigh_kernel<HD>, grid, dim3(kWeighThreads), WeighCfg<HD>::kSmem, s, &cl, map, c, p,
-                                  decay, weight, q_tile));
+                                  decay, weight, q_tile, ranges));
 }
 
 }  // namespace
