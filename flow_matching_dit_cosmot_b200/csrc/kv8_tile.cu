@@ -530,9 +530,11 @@ __global__ void __launch_bounds__(256) tile_join_kernel(const __grid_constant__ 
 // ------------------------------------------------------------------ weighing
 // Warp 0 loads the queries' tiles (TMA), warp 1 issues the products, warps 2-3
 // widen the next item's keys, four warpgroups own the rows of two query tiles
-// x two key tiles.  Items (256 keys of a sequence and key head) go round the
-// CTAs; nothing drains between two items.
+// x two key tiles; warp 3 adds their sums up, two items behind.  Items (256 keys
+// of a sequence and key head) go round the CTAs; nothing drains between two.
+// Registers: 128 x kWeighRegsIo + 512 x kWeighRegsRows out of the launch's pool.
 constexpr int kWeighThreads = 640;
+constexpr int kWeighRegsIo = 64, kWeighRegsRows = 104;
 constexpr int kWeighMaxCluster = 4;
 constexpr int kQSlots = 3;
 constexpr int kPolyPairs = 2;  // of 8 pairs of exponentials, those on the FMA pipe
@@ -574,7 +576,7 @@ __device__ __forceinline__ void exp2_fma(uint64_t x, float& y0, float& y1) {
   x = pack_f32x2(clamp_exp2(a), clamp_exp2(b));
   const uint64_t magic = pack_f32x2(12582912.f, 12582912.f);  // 1.5 * 2^23: the sum's low bits are round(x)
   const uint64_t t = add_f32x2(x, magic);
-  const uint64_t f = add_f32x2(x, neg_f32x2(add_f32x2(t, neg_f32x2(magic))));
+  const uint64_t f = fma_f32x2(add_f32x2(t, pack_f32x2(-12582912.f, -12582912.f)), pack_f32x2(-1.f, -1.f), x);
   uint64_t r = pack_f32x2(kExp2C5, kExp2C5);
   r = fma_f32x2(r, f, pack_f32x2(kExp2C4, kExp2C4));
   r = fma_f32x2(r, f, pack_f32x2(kExp2C3, kExp2C3));
@@ -635,8 +637,10 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   const uint32_t bar_s_empty = bar_s_full + 32;            // [4]
   const uint32_t bar_k_full = bar_s_empty + 32;            // [2]
   const uint32_t bar_k_empty = bar_k_full + 16;            // [2]
-  const uint32_t bar_done = bar_k_empty + 16;              // [1]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kQSlots + 13);
+  const uint32_t bar_sum_full = bar_k_empty + 16;          // [2]
+  const uint32_t bar_sum_empty = bar_sum_full + 16;        // [2]
+  const uint32_t bar_done = bar_sum_empty + 16;            // [1]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kQSlots + 17);
   float* sums = reinterpret_cast<float*>(smem + C::kSums);
   float* parts = reinterpret_cast<float*>(smem + C::kParts);
 
@@ -656,6 +660,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_k_full + 8 * s, 2);
       mbar_init(bar_k_empty + 8 * s, 1);
+      mbar_init(bar_sum_full + 8 * s, 16);
+      mbar_init(bar_sum_empty + 8 * s, 1);
     }
     mbar_init(bar_done, 1);
     fence_barrier_init();
@@ -682,6 +688,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
 
+  if (warp < 4) {
+  setmaxnreg_dec<kWeighRegsIo>();
   if (warp == 0) {
     tma_prefetch_desc(&tmap_q);
     int n = 0;  // tiles so far
@@ -746,15 +754,60 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     }
     umma_commit_if(leader, bar_done);
     warp_wait(bar_done, 0, p.status, kWhereKv8Drain);
-  } else if (warp < 4) {
+  } else {
     // keys to bf16 (exact), rows behind the end zero; the two warps take four (hd 64: eight) rows in turn
     constexpr int kRows = HD == 128 ? 4 : 8, kAhead = 4;
     const int u = HD == 128 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3;
     const int row0 = (warp - 2) * kRows + (HD == 128 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane >> 2);
-    int done = 0;
+    int done = 0, live = 0, added = 0;  // items converted, items with keys, items whose sums were added up
     bool ok = true;
+    WeighItem last[2];
+    // 16 group sums of this CTA, then of the cluster, each added in a fixed order
+    auto add_up = [&](const WeighItem& w, int at) {
+      if (warp == 3) ok = ok && warp_wait(bar_sum_full + 8 * (at & 1), (at >> 1) & 1, p.status, kWhereKv8Softmax);
+      float* my_parts = parts + (at & 1) * kWeighMaxCluster * 16;
+      if (warp == 3) {
+        const float* my_sums = sums + (at & 1) * 128;
+        const int kt = (lane >> 3) & 1, g = lane & 7;
+        float x = 0.f;
+#pragma unroll
+        for (int ph = 0; ph < 2; ++ph)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x += my_sums[((2 * ph + kt) * 4 + q) * 8 + g];
+        if (lane < 16) {
+          if (ranks > 1)
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(my_parts + rank * 16 + lane), 0)),
+                         "f"(x)
+                         : "memory");
+          else
+            my_parts[lane] = x;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_sum_empty + 8 * (at & 1));
+      }
+      if (ranks > 1) cluster_sync();
+      if (warp == 3 && rank == 0 && ok) {
+        const int n_groups = c.block / 16;  // groups of a block
+        const int32_t key = w.k0 + lane * c.block;
+        if (lane < 16 / n_groups && key < w.k_end) {
+          float y = 0.f;
+          for (int r = 0; r < ranks; ++r)
+            for (int e = 0; e < n_groups; ++e) y += my_parts[r * 16 + lane * n_groups + e];
+          const int32_t blk = key / c.block;
+          if (dcheck(blk < c.n_blocks, p.status, kWhereKv8Store)) {
+            float* out = weight + (int64_t)w.bg * c.n_blocks + blk;
+            *out = fmaf(decay, *out, y);
+          }
+        }
+      }
+      __syncwarp();
+    };
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
       const WeighItem w = weigh_item(c, p, item, q_tile, rank, ranks);
+      if (ranks == 1 && live - added == 2) {  // its keys' buffer is free about when its sums are there
+        add_up(last[0], added++);
+        last[0] = last[1];
+      }
       if (w.n_i > 0 && ok) {
         const uint8_t* src = c.k + (int64_t)w.b * c.bstride * c.ld + (int64_t)(w.bg % c.n_kv) * HD + u * 16;
         const uint32_t dst = sK + (done & 1) * 2 * C::kTileBytes;
@@ -791,14 +844,25 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         if (ok && lane == 0) mbar_arrive(bar_k_full + 8 * (done & 1));
         ++done;
       }
-      if (ranks > 1) cluster_sync();
+      if (w.k_end == w.k0) {
+        if (ranks > 1) cluster_sync();
+      } else if (ranks > 1) {
+        add_up(w, live++);
+      } else {
+        last[live - added] = w;
+        ++live;
+      }
     }
+    if (ranks == 1)
+      for (int i = 0; added < live; ++i) add_up(last[i], added++);
+  }
   } else {
+    setmaxnreg_inc<kWeighRegsRows>();
     const int wg = (warp - 4) >> 2, t = wg & 1, phase = wg >> 1;
     const int lane_base = (warp & 3) * 32, row = lane_base + lane;
     const int32_t qr = row / p.group, hr = row % p.group;  // query and head of this row in a tile
     const uint32_t addr = tmem_base + ((uint32_t)lane_base << 16) + 128u * wg;
-    int n = 0, used = 0, parity = 0;  // query tiles, uses of this S buffer, sums' buffer
+    int n = 0, used = 0, done = 0;  // query tiles, uses of this S buffer, items
     bool ok = true;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
       const WeighItem w = weigh_item(c, p, item, q_tile, rank, ranks);
@@ -888,49 +952,17 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         }
       }
       n += w.n_i;
-      // 16 group sums of this CTA, then of the cluster, each added in a fixed order
-      float* my_sums = sums + parity * 128;
+      ok = ok && warp_wait(bar_sum_empty + 8 * (done & 1), ((done >> 1) & 1) ^ 1, p.status, kWhereKv8Softmax);
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) acc[g] += __shfl_xor_sync(0xffffffffu, acc[g], off);
-        if (lane == g) my_sums[(wg * 4 + (warp & 3)) * 8 + g] = acc[g];
+        if (lane == g) sums[(done & 1) * 128 + (wg * 4 + (warp & 3)) * 8 + g] = acc[g];
       }
-      asm volatile("bar.sync 1, 512;" ::: "memory");  // the four warpgroups of rows
-      float* my_parts = parts + parity * kWeighMaxCluster * 16;
-      if (warp == 4) {
-        const int kt = (lane >> 3) & 1, g = lane & 7;
-        float x = 0.f;
-#pragma unroll
-        for (int ph = 0; ph < 2; ++ph)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) x += my_sums[((2 * ph + kt) * 4 + q) * 8 + g];
-        if (lane < 16) {
-          const uint32_t at = smem_u32(my_parts + rank * 16 + lane);
-          if (ranks > 1)
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(at, 0)), "f"(x) : "memory");
-          else
-            my_parts[lane] = x;
-        }
-        __syncwarp();
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_sum_full + 8 * (done & 1));
+      ++done;
       if (ranks > 1) cluster_sync();
-      if (warp == 4 && rank == 0) {
-        const int n_groups = c.block / 16;  // groups of a block
-        const int32_t key = w.k0 + lane * c.block;
-        if (lane < 16 / n_groups && key < w.k_end) {
-          float x = 0.f;
-          for (int r = 0; r < ranks; ++r)
-            for (int g = 0; g < n_groups; ++g) x += my_parts[r * 16 + lane * n_groups + g];
-          const int32_t blk = key / c.block;
-          if (dcheck(blk < c.n_blocks, p.status, kWhereKv8Store)) {
-            float* out = weight + (int64_t)w.bg * c.n_blocks + blk;
-            *out = fmaf(decay, *out, x);
-          }
-        }
-        __syncwarp();
-      }
-      parity ^= 1;
     }
   }
   tc_fence_before();
@@ -970,8 +1002,8 @@ size_t plan_o_bytes(const TilePlan& t, int hd) {
   return ((size_t)t.splits * t.n_tail * 2 * kTile * hd * 4 + 255) & ~size_t(255);
 }
 
-// Sets a kernel's shared-memory limit once per device; `regs`, if not 0, is
-// the sum that its register hand-over needs of the launch.
+// Sets a kernel's shared-memory limit once per device; `regs` is the sum that
+// its register hand-over needs of the launch.
 template <typename K>
 cosmot_status prepare(K kern, int smem, int64_t regs, int threads, uint64_t& done) {
   static std::mutex mu;
@@ -980,11 +1012,9 @@ cosmot_status prepare(K kern, int smem, int64_t regs, int threads, uint64_t& don
   std::lock_guard<std::mutex> lk(mu);
   if (dev < 64 && (done & (1ull << dev))) return COSMOT_OK;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return COSMOT_ERR_CUDA;
-  if (regs) {
-    // a build whose register count cannot fund the hand-over is not launched
-    cudaFuncAttributes fa{};
-    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || regs > (int64_t)threads * fa.numRegs) return COSMOT_ERR_CUDA;
-  }
+  // a build whose register count cannot fund the hand-over is not launched
+  cudaFuncAttributes fa{};
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || regs > (int64_t)threads * fa.numRegs) return COSMOT_ERR_CUDA;
   if (dev < 64) done |= 1ull << dev;
   return COSMOT_OK;
 }
@@ -1015,7 +1045,8 @@ cosmot_status launch_attention(const Cache& c, const Query& p, const TilePlan& t
 template <int HD>
 cosmot_status launch_weigh(const Cache& c, const Query& p, float decay, float* weight, int32_t max_len, cudaStream_t s) {
   static uint64_t done = 0;
-  cosmot_status st = prepare(tile_weigh_kernel<HD>, WeighCfg<HD>::kSmem, 0, kWeighThreads, done);
+  cosmot_status st = prepare(tile_weigh_kernel<HD>, WeighCfg<HD>::kSmem, 128 * kWeighRegsIo + 512 * kWeighRegsRows,
+                             kWeighThreads, done);
   if (st != COSMOT_OK) return st;
   const int32_t q_tile = kTile / p.group;
   CUtensorMap map;

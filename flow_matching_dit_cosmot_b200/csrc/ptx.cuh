@@ -445,8 +445,6 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
-__device__ __forceinline__ uint64_t neg_f32x2(uint64_t v) { return v ^ 0x8000000080000000ull; }
-
 // 2^x on the SFU (PTX ex2.approx, flush-to-zero).
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
