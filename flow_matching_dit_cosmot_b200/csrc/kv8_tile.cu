@@ -46,8 +46,9 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
 }
 
 // Byte offset of 16-byte piece `piece` (of 8 columns) of `row` in a tile of boxes of 64 columns.
+template <int BOX = kBoxBytes>
 __device__ __forceinline__ uint32_t sw_offset(int row, int piece) {
-  return (uint32_t)((piece >> 3) * kBoxBytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+  return (uint32_t)((piece >> 3) * BOX + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -546,7 +547,9 @@ struct WeighCfg {
   static constexpr int kSums = kBars + 192;                 // [2][4 warpgroups][4 warps][8 groups]
   static constexpr int kParts = kSums + 2 * 4 * 4 * 8 * 4;  // [2][cluster][16 groups]
   static constexpr int kSmem = kParts + 2 * kWeighMaxCluster * 16 * 4 + 1024;
-  static constexpr uint32_t kIdesc = idesc_bf16_f32(kTile, kTile, false, false);
+  static constexpr int kBoxK = 2 * kBoxBytes;  // 256 keys x 64 columns
+  static constexpr uint32_t kIdesc2 = idesc_bf16_f32(kTile, 2 * kTile, false, false);  // both key tiles at once
+  static constexpr uint32_t kIdesc1 = idesc_bf16_f32(kTile, kTile, false, false);
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
@@ -633,14 +636,14 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
   const uint32_t bar_q_full = smem_u32(bars);              // [kQSlots]
   const uint32_t bar_q_empty = bar_q_full + 8 * kQSlots;   // [kQSlots]
-  const uint32_t bar_s_full = bar_q_empty + 8 * kQSlots;   // [4]
-  const uint32_t bar_s_empty = bar_s_full + 32;            // [4]
-  const uint32_t bar_k_full = bar_s_empty + 32;            // [2]
+  const uint32_t bar_s_full = bar_q_empty + 8 * kQSlots;   // [2]
+  const uint32_t bar_s_empty = bar_s_full + 16;            // [2]
+  const uint32_t bar_k_full = bar_s_empty + 16;            // [2]
   const uint32_t bar_k_empty = bar_k_full + 16;            // [2]
   const uint32_t bar_sum_full = bar_k_empty + 16;          // [2]
   const uint32_t bar_sum_empty = bar_sum_full + 16;        // [2]
   const uint32_t bar_done = bar_sum_empty + 16;            // [1]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kQSlots + 17);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kQSlots + 13);
   float* sums = reinterpret_cast<float*>(smem + C::kSums);
   float* parts = reinterpret_cast<float*>(smem + C::kParts);
 
@@ -653,11 +656,9 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       mbar_init(bar_q_full + 8 * s, 1);
       mbar_init(bar_q_empty + 8 * s, 1);
     }
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(bar_s_full + 8 * s, 1);
-      mbar_init(bar_s_empty + 8 * s, 4);
-    }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(bar_s_full + 8 * s, 1);
+      mbar_init(bar_s_empty + 8 * s, 8);
       mbar_init(bar_k_full + 8 * s, 2);
       mbar_init(bar_k_empty + 8 * s, 1);
       mbar_init(bar_sum_full + 8 * s, 16);
@@ -719,33 +720,28 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     const uint32_t leader = elect_one();
-    int n = 0, used[2][2] = {{0, 0}, {0, 0}}, done = 0;  // query tiles; uses of S buffer [phase][key tile]; items
+    int n = 0, done = 0;  // query tiles, items
     bool ok = true;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
       const WeighItem w = weigh_item(c, p, item, q_tile, rank, ranks);
       if (w.n_i > 0 && ok) {
         const int kbuf = done & 1;
+        const uint32_t idesc = w.two ? C::kIdesc2 : C::kIdesc1;
+        const uint32_t ka = sw128_desc_lo(sK + 2 * kbuf * C::kTileBytes, 16);
         ok = warp_wait(bar_k_full + 8 * kbuf, (done >> 1) & 1, p.status, kWhereKv8Mma);
         for (int i = 0; i < w.n_i && ok; ++i, ++n) {
           const int slot = n % kQSlots, phase = n & 1;
-          ok = warp_wait(bar_q_full + 8 * slot, (n / kQSlots) & 1, p.status, kWhereKv8Mma);
+          ok = warp_wait(bar_q_full + 8 * slot, (n / kQSlots) & 1, p.status, kWhereKv8Mma) &&
+               warp_wait(bar_s_empty + 8 * phase, ((n >> 1) & 1) ^ 1, p.status, kWhereKv8Mma);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t qa = sw128_desc_lo(sQ + slot * C::kTileBytes, 16);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!ok || (t == 1 && !w.two)) break;
-            const int buf = 2 * phase + t, u = phase ? used[1][t]++ : used[0][t]++;
-            ok = warp_wait(bar_s_empty + 8 * buf, (u & 1) ^ 1, p.status, kWhereKv8Mma);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t qa = sw128_desc_lo(sQ + slot * C::kTileBytes, 16);
-            const uint32_t ka = sw128_desc_lo(sK + (2 * kbuf + t) * C::kTileBytes, 16);
-#pragma unroll
-            for (int k = 0; k < HD / 16; ++k) {
-              const uint32_t off = ((k >> 2) * kBoxBytes + (k & 3) * 32) >> 4;
-              umma_ss_lo(leader, tmem_base + 128u * buf, qa + off, ka + off, C::kIdesc, k > 0 ? 1u : 0u);
-            }
-            umma_commit_if(leader, bar_s_full + 8 * buf);
-          }
-          if (ok) umma_commit_if(leader, bar_q_empty + 8 * slot);
+          for (int k = 0; k < HD / 16; ++k)
+            umma_ss_lo(leader, tmem_base + 256u * phase, qa + (((k >> 2) * kBoxBytes + (k & 3) * 32) >> 4),
+                       ka + (((k >> 2) * C::kBoxK + (k & 3) * 32) >> 4), idesc, k > 0 ? 1u : 0u);
+          umma_commit_if(leader, bar_s_full + 8 * phase);
+          umma_commit_if(leader, bar_q_empty + 8 * slot);
         }
         if (ok) umma_commit_if(leader, bar_k_empty + 8 * kbuf);
         ++done;
@@ -834,9 +830,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
               y[2 * e] = pack_bf16x2(f0.x, f0.y);
               y[2 * e + 1] = pack_bf16x2(f1.x, f1.y);
             }
-            const uint32_t d = dst + (row >> 7) * C::kTileBytes;
-            st_shared16(d + sw_offset(row & 127, 2 * u), y[0], y[1], y[2], y[3]);
-            st_shared16(d + sw_offset(row & 127, 2 * u + 1), y[4], y[5], y[6], y[7]);
+            st_shared16(dst + sw_offset<C::kBoxK>(row, 2 * u), y[0], y[1], y[2], y[3]);
+            st_shared16(dst + sw_offset<C::kBoxK>(row, 2 * u + 1), y[4], y[5], y[6], y[7]);
           }
         }
         fence_proxy_async_smem();
@@ -862,7 +857,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     const int lane_base = (warp & 3) * 32, row = lane_base + lane;
     const int32_t qr = row / p.group, hr = row % p.group;  // query and head of this row in a tile
     const uint32_t addr = tmem_base + ((uint32_t)lane_base << 16) + 128u * wg;
-    int n = 0, used = 0, done = 0;  // query tiles, uses of this S buffer, items
+    int n = 0, done = 0;  // query tiles, items
     bool ok = true;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
       const WeighItem w = weigh_item(c, p, item, q_tile, rank, ranks);
@@ -879,30 +874,32 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         f[g] = key < w.k_end ? p.scale_log2 * __ldg(c.k_scale + (int64_t)w.bg * c.n_blocks + key / c.block) : 0.f;
       }
       const float* lse_row = p.lse + ((int64_t)w.b * p.n_heads + (w.bg % c.n_kv) * p.group + hr) * p.n_q;
-      if (t == 0 || w.two) {
-#pragma unroll 1
-        for (int i = (phase ^ n) & 1; i < w.n_i && ok; i += 2) {
+      {
+        // rows that are not there weigh 2^-inf; a tile's lse is loaded one tile ahead
+        auto load_lse = [&](int i) {
           const int64_t qi = (int64_t)(w.i0 + i) * q_tile + qr;
-          // rows that are not there weigh 2^-inf; rows that saw nothing (lse = -inf) are hidden from every key
-          float ls = INFINITY;
+          return row < tile_rows && qi < p.n_q ? __ldg(lse_row + qi) : INFINITY;
+        };
+        const int first = (phase ^ n) & 1;
+        float ls_next = first < w.n_i ? load_lse(first) : 0.f;
+#pragma unroll 1
+        for (int i = first; i < w.n_i && ok; i += 2) {
+          const float ls = ls_next * kLog2e;
+          if (i + 2 < w.n_i) ls_next = load_lse(i + 2);
           int32_t lim = w.k_end;
-          if (row < tile_rows && qi < p.n_q) {
-            ls = __ldg(lse_row + qi) * kLog2e;
-            if (p.causal) {
-              const int64_t x = (int64_t)w.len - p.n_q + qi + 1;
-              lim = x < 0 ? 0 : (x < w.k_end ? (int32_t)x : w.k_end);
-            }
-            if (ls == -INFINITY) lim = 0;
+          if (p.causal) {
+            const int64_t x = (int64_t)w.len - p.n_q + (int64_t)(w.i0 + i) * q_tile + qr + 1;
+            lim = x < 0 ? 0 : (x < w.k_end ? (int32_t)x : w.k_end);
           }
+          if (ls == -INFINITY) lim = 0;  // a row that saw nothing is hidden from every key
           const bool masked = kbase + kTile > lim;
-          const bool any = __any_sync(0xffffffffu, lim > kbase);
-          ok = warp_wait(bar_s_full + 8 * wg, used & 1, p.status, kWhereKv8Softmax);
-          ++used;
+          const bool any = __any_sync(0xffffffffu, lim > kbase);  // (no key of a tile behind the end)
+          ok = warp_wait(bar_s_full + 8 * phase, ((n + i) >> 1) & 1, p.status, kWhereKv8Softmax);
           if (!ok) break;
           tc_fence_after();
           if (!any) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_s_empty + 8 * wg);
+            if (lane == 0) mbar_arrive(bar_s_empty + 8 * phase);
             continue;
           }
           uint32_t s[2][32];
@@ -915,7 +912,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
             } else {  // S is in registers: the next product may overwrite it
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(bar_s_empty + 8 * wg);
+              if (lane == 0) mbar_arrive(bar_s_empty + 8 * phase);
             }
             uint32_t(&x)[32] = s[q & 1];
             if (masked) {
