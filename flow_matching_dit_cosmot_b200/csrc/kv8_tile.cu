@@ -978,16 +978,16 @@ TilePlan make_plan(const Cache& c, const Query& p, int32_t max_len) {
   const int64_t n_kt = ((int64_t)max_len + kTile - 1) / kTile;
   t.splits = 1;
   t.n_full = (int32_t)items;
-  // Items of a last wave that does not fill the SMs are split over the keys so
-  // that it does (items of a single query tile take about half as long).
+  // Items of a last wave that does not fill the SMs are split over the keys, the
+  // way that takes the fewest key tiles in turn; a CTA's start and end cost it
+  // about four more, and joining a split about one for every 64 items.
   const int64_t tail = items % sms;
-  const bool single = (p.n_rows - 1) % (2 * kTile) < kTile;
-  const double load = (double)tail - (single && !p.causal ? 0.45 * (double)(tail < heads ? tail : heads) : 0.0);
-  if (tail > 0) {
-    int64_t s = (int64_t)((double)sms / load + 0.25);
-    if (s > n_kt / 2) s = n_kt / 2;
-    if (s > 1) {
-      t.splits = (int32_t)s;
+  double best = (double)(n_kt + 4);
+  for (int64_t k = 2; tail > 0 && k <= 32 && 2 * k <= n_kt; ++k) {
+    const double cost = (double)((tail * k + sms - 1) / sms) * ((double)((n_kt + k - 1) / k) + 4) + (double)(tail * k) / 64 + 2;
+    if (cost < best) {
+      best = cost;
+      t.splits = (int32_t)k;
       t.n_tail = (int32_t)tail;
       t.n_full = (int32_t)(items - tail);
     }
