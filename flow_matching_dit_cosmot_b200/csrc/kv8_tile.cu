@@ -55,6 +55,13 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// 32 bytes to a 32-byte-aligned address.
+__device__ __forceinline__ void st_global32(void* dst, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* status, int where) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, where));
 }
@@ -76,7 +83,8 @@ template <int HD>
 struct AttnCfg {
   static constexpr int kTileBytes = kTile * HD * 2;
   static constexpr int kScaleBytes = 4 * 8 * 16;  // four key tiles in flight, eight groups each
-  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 256 + kScaleBytes + 1024;
+  static constexpr int kFacBytes = 2 * kTile * 4;  // the query rows' factors
+  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 256 + kScaleBytes + kFacBytes + 1024;
   static constexpr uint32_t kIdescS = idesc_f16_f32(kTile, kTile, false);
   static constexpr uint32_t kIdescO = idesc_f16_f32(kTile, HD, true);
   __device__ static constexpr uint32_t s_col(int t) { return (uint32_t)t * 128u; }
@@ -104,6 +112,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 1 + 2 * kSlots + 7);
   // [4][NG] (ks, log2 vs, 1/vs)
   float4* scales = reinterpret_cast<float4*>(smem + (2 + kSlots) * C::kTileBytes + 256);
+  float* facs = reinterpret_cast<float*>(smem + (2 + kSlots) * C::kTileBytes + 256 + C::kScaleBytes);
   constexpr int kGroupKeys = kTile / NG;
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
@@ -294,50 +303,54 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int lane_base = (warp & 3) * 32;   // TMEM lanes this warp may access
     const int64_t r = r0 + t * kTile + lane_base + lane;
     const bool valid = r < p.n_rows;
-    const int64_t qi = valid ? r / p.group : 0;
-    const int32_t h = kvh * p.group + (int32_t)(valid ? r % p.group : 0);
-    float fac = p.scale_log2;
+    const int32_t qi = valid ? (int32_t)((uint32_t)r / (uint32_t)p.group) : 0;
+    const int32_t h = kvh * p.group + (valid ? (int32_t)r - qi * p.group : 0);
+    // Q: a warp's 32 rows, 16 bytes a lane, several whole rows at a time
     if (n_vis > 0 && (t == 0 || two)) {
-      const uint4* q4 = reinterpret_cast<const uint4*>(p.q + (b * p.q_bstride + qi) * p.ld_q + (int64_t)h * HD);
-      uint4 x[HD / 8];
-      float amax = 0.f;
-      bool finite = true;
-#pragma unroll
-      for (int i = 0; i < HD / 8; ++i) {
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (valid) x[i] = __ldg(q4 + i);
-      }
-#pragma unroll
-      for (int i = 0; i < HD / 8; ++i) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 v = unpack_bf16x2(w[e]);
-          amax = fmax3(amax, fabsf(v.x), fabsf(v.y));
-          finite = finite && fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY;
-        }
-      }
-      // below 2^-47 a row loses bits of less than 2^-85: nothing that a key could raise to a visible score
-      int e2 = (int)((__float_as_uint(amax) >> 23) & 255u) - 127 - 13;
-      e2 = e2 < -60 ? -60 : (e2 > 114 ? 114 : e2);
-      const float down = exp2_int(-e2);
-      fac = finite ? fmaxf(p.scale_log2 * exp2_int(e2), 1e-25f) : __int_as_float(0x7fc00000);
+      constexpr int kLanes = HD / 8, kRows = 32 / kLanes;  // lanes of a row, rows of one load
+      const int64_t at = (int64_t)(b * p.q_bstride + qi) * p.ld_q + (int64_t)h * HD;  // this lane's own row
       const uint32_t dst = sQ + t * C::kTileBytes;
+      const int piece = lane % kLanes;
+      uint4 x[32 / kRows];
 #pragma unroll
-      for (int i = 0; i < HD / 8; ++i) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i]);
-        uint32_t y[4];
+      for (int i = 0; i < 32 / kRows; ++i) {
+        const int row = i * kRows + lane / kLanes;
+        const int64_t from = __shfl_sync(0xffffffffu, at, row);
+        const bool live = __shfl_sync(0xffffffffu, (int)valid, row) != 0;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (live) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + from) + piece);
+      }
+      {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 v = unpack_bf16x2(w[e]);
-          y[e] = pack_f16x2(v.x * down, v.y * down);
+        for (int i = 0; i < 32 / kRows; ++i) {
+          const int row = i * kRows + lane / kLanes;
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i]);
+          // magnitudes of bf16 order like their bits
+          uint32_t mag = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+#pragma unroll
+          for (int off = 1; off < kLanes; off <<= 1) mag = __vmaxu2(mag, __shfl_xor_sync(0xffffffffu, mag, off));
+          mag = max(mag & 0xffffu, mag >> 16);
+          // below 2^-47 a row loses bits of less than 2^-85: nothing that a key could raise to a visible score
+          int e2 = (int)(mag >> 7) - 127 - 13;
+          e2 = e2 < -60 ? -60 : (e2 > 114 ? 114 : e2);
+          const float down = exp2_int(-e2);
+          if (piece == 0)
+            facs[t * kTile + lane_base + row] =
+                mag < 0x7f80u ? fmaxf(p.scale_log2 * exp2_int(e2), 1e-25f) : __int_as_float(0x7fc00000);
+          uint32_t y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = unpack_bf16x2(w[e]);
+            y[e] = pack_f16x2(v.x * down, v.y * down);
+          }
+          st_shared16(dst + sw_offset(lane_base + row, piece), y[0], y[1], y[2], y[3]);
         }
-        st_shared16(dst + sw_offset(lane_base + lane, i), y[0], y[1], y[2], y[3]);
       }
       fence_proxy_async_smem();
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_q);
+    const float fac = facs[t * kTile + lane_base + lane];
 
     const uint32_t s_addr = tmem_base + ((uint32_t)lane_base << 16) + C::s_col(t);
     const uint32_t o_addr = tmem_base + ((uint32_t)lane_base << 16) + C::o_col(t);
@@ -467,6 +480,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       __nv_bfloat16* dst = p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD;
       float* pdst = p.part_o + pr * HD;
+      const bool wide = (((uintptr_t)p.o | (uintptr_t)(p.ld_o * 2)) & 31) == 0;  // whole sectors: 32 bytes a store
       if (ok) {
 #pragma unroll 1
         for (int i = 0; i < HD / 32; ++i) {
@@ -480,17 +494,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : __uint_as_float(ov[e]) * inv;
           if (store && splits > 1) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<float4*>(pdst + 32 * i + 4 * e) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) st_global32(pdst + 32 * i + 8 * e, reinterpret_cast<const uint32_t*>(v) + 8 * e);
           } else if (store) {
+            uint32_t y[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint4 x;
-              x.x = pack_bf16x2(v[8 * e], v[8 * e + 1]);
-              x.y = pack_bf16x2(v[8 * e + 2], v[8 * e + 3]);
-              x.z = pack_bf16x2(v[8 * e + 4], v[8 * e + 5]);
-              x.w = pack_bf16x2(v[8 * e + 6], v[8 * e + 7]);
-              *reinterpret_cast<uint4*>(dst + 32 * i + 8 * e) = x;
+            for (int e = 0; e < 16; ++e) y[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+            if (wide) {
+              st_global32(dst + 32 * i, y);
+              st_global32(dst + 32 * i + 16, y + 8);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4*>(dst + 32 * i + 8 * e) = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
             }
           }
         }
