@@ -159,12 +159,12 @@ struct Ring {
   static constexpr int kPieceK = 512;               // 16 bytes a lane
   static constexpr int kPieceV = HD == 128 ? 512 : 256;
   static constexpr int kOffV = 2 * (HD / 64) * kPieceK;
-  static constexpr int kOffS = kOffV + 4 * kPieceV;  // ks, vs: 4 bytes a lane each
-  static constexpr int kStage = kOffS + 256;
+  static constexpr int kStage = kOffV + 4 * kPieceV;
+  static constexpr int kScales = 256;               // blocks whose scales are kept in shared memory
   static constexpr int kRowPitch = HD + 4;           // floats between rows of the warps' parts
   static constexpr int smem(int nt) {
     const int ring = kWarps * kRing * kStage, parts = kWarps * 8 * nt * (kRowPitch * 4 + 8);
-    return ring > parts ? ring : parts;
+    return kScales * 16 + (ring > parts ? ring : parts);
   }
 };
 
@@ -198,7 +198,11 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) rows_attention_kernel
   const float* ksp = c.k_scale + (int64_t)blockIdx.z * c.n_blocks;
   const float* vsp = c.v_scale + (int64_t)blockIdx.z * c.n_blocks;
   const int block_shift = 31 - __clz(c.block);
-  const uint32_t ring = smem_u32(sm_raw) + warp * kRing * R::kStage;
+  float4* scales = reinterpret_cast<float4*>(sm_raw);  // (ks, log2 vs, 1/vs)
+  const uint32_t ring = smem_u32(sm_raw) + R::kScales * 16 + warp * kRing * R::kStage;
+  // V pieces: a row's eight pieces side by side, turned by the row so that the
+  // lanes' reads fall on all banks too
+  const uint32_t v_at = R::kOffV + (uint32_t)(j * 8 + (g ^ (2 * j))) * (HD / 8);
 
   auto fetch = [&](int32_t key0, int slot) {
     if (key0 < kend) {
@@ -215,12 +219,9 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) rows_attention_kernel
       for (int s = 0; s < 4; ++s) {
         const int32_t key = key0 + 8 * (s >> 1) + 2 * j + (s & 1);
         const bool live = key < kend;
-        cp_async<HD / 8>(ring + slot * R::kStage + R::kOffV + s * R::kPieceV + lane * (HD / 8),
-                         vb + (int64_t)(live ? key : key0) * c.ld + g * (HD / 8), live);
+        cp_async<HD / 8>(ring + slot * R::kStage + v_at + s * R::kPieceV, vb + (int64_t)(live ? key : key0) * c.ld + g * (HD / 8),
+                         live);
       }
-      const uint32_t sc = ring + slot * R::kStage + R::kOffS + lane * 8;
-      cp_async<4>(sc, ksp + (key0 >> block_shift), true);
-      cp_async<4>(sc + 4, vsp + (key0 >> block_shift), true);
     }
     cp_async_commit();  // a group per stage, whether it holds anything or not
   };
@@ -228,6 +229,15 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) rows_attention_kernel
   const int32_t first = k0 + 16 * warp;
 #pragma unroll
   for (int i = 0; i < kRing - 1; ++i) fetch(first + i * kStep, i);
+  auto scale_of = [&](int32_t blk) {
+    float4 s;
+    s.x = __ldg(ksp + blk);
+    scale_log2_parts(__ldg(vsp + blk), s.y, s.z);
+    s.w = 0.f;
+    return s;
+  };
+  const int32_t blk0 = k0 >> block_shift, blk1 = ((kend - 1) >> block_shift) + 1;
+  for (int32_t i = blk0 + (int32_t)threadIdx.x; i < min(blk1, blk0 + R::kScales); i += 32 * kWarps) scales[i - blk0] = scale_of(i);
 
   uint32_t q[NT][HD / 16][2];
   float fac[NT][2];
@@ -257,6 +267,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) rows_attention_kernel
     l[n][0] = l[n][1] = 0.f;
   }
 
+  __syncthreads();  // the scales
   int slot = 0;
 #pragma unroll 1
   for (int32_t key0 = first; key0 < kend; key0 += kStep) {
@@ -270,10 +281,9 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) rows_attention_kernel
       ka[h] = ld_shared16(st + h * R::kPieceK + lane * 16);
       kc[h] = ld_shared16(st + (HD / 64 + h) * R::kPieceK + lane * 16);
     }
-    const uint2 sc = ld_shared8(st + R::kOffS + lane * 8);
-    const float ks = __uint_as_float(sc.x);
-    float vlog, vinv;
-    scale_log2_parts(__uint_as_float(sc.y), vlog, vinv);
+    const int32_t blk = key0 >> block_shift;
+    const float4 sc = blk - blk0 < R::kScales ? scales[blk - blk0] : scale_of(blk);
+    const float ks = sc.x, vlog = sc.y, vinv = sc.z;
 
     float s[NT][4];
     scores<HD, NT>(s, ka, kc, q);
@@ -327,7 +337,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) rows_attention_kernel
     uint32_t vw[4][VW];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t at = st + R::kOffV + k * R::kPieceV + lane * (HD / 8);
+      const uint32_t at = st + v_at + k * R::kPieceV;
       if constexpr (HD == 128) {
         *reinterpret_cast<uint4*>(vw[k]) = ld_shared16(at);
       } else {
@@ -352,7 +362,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) rows_attention_kernel
   __syncthreads();  // the ring's memory takes the warps' parts now
 
   // lane (g, j): rows 2j, 2j + 1 of each tile, dims hd/8 g + (2i, 2i + 1)
-  float* sm_o = reinterpret_cast<float*>(sm_raw);
+  float* sm_o = reinterpret_cast<float*>(sm_raw + R::kScales * 16);
   float2* sm_ml = reinterpret_cast<float2*>(sm_o + kWarps * 8 * NT * R::kRowPitch);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -488,14 +498,12 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
 // ------------------------------------------------------------------ weighing
 // A warp owns whole blocks of rows and sums 2^(s - lse) over their keys and
 // eight NT query rows, so that nothing is added by two threads.  The keys, the
-// blocks' scales and their old weights come through a ring of 16-key stages, as
-// above.  More query rows take more passes over the keys (from L2).
+// keys come through a ring of 16-key stages, as above.  More query rows take more passes over the keys (from L2).
 constexpr int kWeighRing = 5;
 
 template <int HD>
 struct WeighRing {
-  static constexpr int kOffS = 2 * (HD / 64) * 512;  // ks and the old weight: 4 bytes a lane each
-  static constexpr int kStage = kOffS + 256;
+  static constexpr int kStage = 2 * (HD / 64) * 512;
   static constexpr int kSmem = kWarps * kWeighRing * kStage;
 };
 
@@ -533,9 +541,6 @@ __global__ void __launch_bounds__(32 * kWarps) rows_weigh_kernel(const __grid_co
 #pragma unroll
         for (int h = 0; h < HD / 64; ++h) cp_async<16>(st + (i * (HD / 64) + h) * 512, src + 64 * h, live);
       }
-      const uint32_t sc = ring + slot * R::kStage + R::kOffS + lane * 8;
-      cp_async<4>(sc, ksp + blk, true);
-      cp_async<4>(sc + 4, wp + blk, true);
     }
     cp_async_commit();
   };
@@ -564,10 +569,21 @@ __global__ void __launch_bounds__(32 * kWarps) rows_weigh_kernel(const __grid_co
       }
     lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 1));
     lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 2));
-    float sum = 0.f;
+    float sum = 0.f, ks = 0.f, before = 0.f;
+    // a block's scale and old weight are loaded one block ahead
+    float ks_next = __ldg(ksp + blk0), before_next = wp[blk0];
     int slot = 0;
 #pragma unroll 1
     for (int t = 0; t < n; ++t) {
+      if ((t & (stages - 1)) == 0) {
+        ks = ks_next;
+        before = before_next;
+        const int32_t ahead = blk0 + ((t >> shift) + 1) * kWarps;
+        if (ahead < blk1) {
+          ks_next = __ldg(ksp + ahead);
+          before_next = wp[ahead];
+        }
+      }
       fetch(t + kWeighRing - 1, slot == 0 ? kWeighRing - 1 : slot - 1);
       cp_async_wait<kWeighRing - 1>();
       const uint32_t st = ring + slot * R::kStage;
@@ -578,8 +594,6 @@ __global__ void __launch_bounds__(32 * kWarps) rows_weigh_kernel(const __grid_co
         ka[h] = ld_shared16(st + h * 512 + lane * 16);
         kc[h] = ld_shared16(st + (HD / 64 + h) * 512 + lane * 16);
       }
-      const uint2 sc = ld_shared8(st + R::kOffS + lane * 8);
-      const float ks = __uint_as_float(sc.x);
       const int32_t blk = blk0 + (t >> shift) * kWarps, key0 = blk * c.block + (t & (stages - 1)) * 16;
       float s[NT][4];
       scores<HD, NT>(s, ka, kc, q);
@@ -594,9 +608,9 @@ __global__ void __launch_bounds__(32 * kWarps) rows_weigh_kernel(const __grid_co
       if ((t & (stages - 1)) == stages - 1) {  // the block's last keys
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        // (a later pass reads what lane 0 wrote here itself: through its own copy)
+        // (in a later pass lane 0 reads back what it wrote in the one before)
         if (lane == 0 && dcheck(blk < c.n_blocks, p.status, kWhereKv8Store))
-          wp[blk] = r0 == 0 ? fmaf(decay, __uint_as_float(sc.y), sum) : wp[blk] + sum;
+          wp[blk] = fmaf(r0 == 0 ? decay : 1.f, before, sum);
         sum = 0.f;
       }
     }
