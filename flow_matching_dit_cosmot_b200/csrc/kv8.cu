@@ -16,13 +16,23 @@ namespace kv8 {
 // bound: HBM (4 bytes read and 2 written for each K and V element).
 constexpr int kStoreThreads = 256;
 
+// Largest of the CTA's values: magnitudes of bf16 order like their bits.
+__device__ __forceinline__ uint32_t cta_max_bf16(uint32_t mag, uint32_t* part) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) mag = __vmaxu2(mag, __shfl_xor_sync(0xffffffffu, mag, off));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = mag;
+  __syncthreads();
+  for (int i = 0; i < (int)blockDim.x >> 5; ++i) mag = __vmaxu2(mag, part[i]);
+  return max(mag & 0xffffu, mag >> 16);
+}
+
 template <int kUnits>
 __global__ void __launch_bounds__(kStoreThreads, 3)
     store_kernel(const __grid_constant__ Cache c, const __nv_bfloat16* __restrict__ ksrc,
                  const __nv_bfloat16* __restrict__ vsrc, int64_t ld_src, int64_t src_bstride, int32_t n, int* status) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float part[kStoreThreads / 32];
+  __shared__ uint32_t part[2][kStoreThreads / 32];
   const uint32_t sides = 2u * c.batch * c.n_kv;  // K and V of every head
   const uint32_t side = blockIdx.x % sides;
   const bool is_v = side & 1;
@@ -45,7 +55,6 @@ __global__ void __launch_bounds__(kStoreThreads, 3)
   float* scale = (is_v ? c.v_scale : c.k_scale) + (int64_t)bg * c.n_blocks + blk;
 
   uint4 x[kUnits];
-  float amax = 0.f;
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
     const int32_t row = first + u * step;
@@ -53,23 +62,26 @@ __global__ void __launch_bounds__(kStoreThreads, 3)
     if (row >= held && row < end) x[u] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(u * step) * ld_src));
   }
   const float old = row0 < held ? *scale : 0.f;  // read by every thread before thread 0 writes it
+  uint32_t mag = 0;
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[u]);
+  for (int u = 0; u < kUnits; ++u)
+    mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(x[u].x & 0x7fff7fffu, x[u].y & 0x7fff7fffu),
+                                 __vmaxu2(x[u].z & 0x7fff7fffu, x[u].w & 0x7fff7fffu)));
+  mag = cta_max_bf16(mag, part[0]);
+  if (mag >= 0x7f80u) {  // infinities saturate like any other large value and NaN stays NaN: neither sets the scale
+    mag = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack_bf16x2(w[i]);
-      // infinities saturate like any other large value and NaN stays NaN: neither sets the scale
-      const float a = fabsf(f.x), d = fabsf(f.y);
-      if (a < INFINITY) amax = fmaxf(amax, a);
-      if (d < INFINITY) amax = fmaxf(amax, d);
+    for (int u = 0; u < kUnits; ++u) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[u]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a = w[i] & 0x7fff7fffu;
+        mag = __vmaxu2(mag, a & ~__vcmpgeu2(a, 0x7f807f80u));
+      }
     }
+    mag = cta_max_bf16(mag, part[1]);
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
-  __syncthreads();
-  for (int i = 0; i < (int)blockDim.x >> 5; ++i) amax = fmaxf(amax, part[i]);
+  const float amax = __uint_as_float(mag << 16);
   const float fresh = exp2_int(scale_exponent(amax));
   const bool have_old = old > 0.f && old < INFINITY;
   const float now = have_old && old > fresh ? old : fresh;

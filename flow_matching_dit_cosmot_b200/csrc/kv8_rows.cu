@@ -29,8 +29,8 @@ namespace kv8 {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kRing = 4;       // stages of 16 keys in flight
-constexpr int kCtasPerSm = 3;  // shared memory and registers allow three
+constexpr int kRing = 3;  // stages of 16 keys
+constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : 3; }  // shared memory and registers allow
 constexpr float kPBias = 8.f, kFollow = 7.f;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -171,7 +171,7 @@ struct Ring {
 // One CTA per (key range, 8 NT packed rows, sequence and key head); its warps
 // take 16 keys in turn.
 template <int HD, int NT>
-__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) rows_attention_kernel(const __grid_constant__ Cache c,
+__global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_kernel(const __grid_constant__ Cache c,
                                                                                  const __grid_constant__ Query p) {
   pdl_trigger();
   pdl_wait();
@@ -497,8 +497,9 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
 
 // ------------------------------------------------------------------ weighing
 // A warp owns whole blocks of rows and sums 2^(s - lse) over their keys and
-// eight NT query rows, so that nothing is added by two threads.  The keys, the
-// keys come through a ring of 16-key stages, as above.  More query rows take more passes over the keys (from L2).
+// eight NT query rows, so that nothing is added by two threads.  The keys come
+// through a ring of 16-key stages, as above.  More query rows take more passes
+// over the keys (from L2).
 constexpr int kWeighRing = 5;
 
 template <int HD>
@@ -648,7 +649,7 @@ void rows_plan(const Cache& c, Query& p, int32_t max_len) {
   if (tiles <= 0) return;
   // as many key ranges as fill the SMs once (a batch of unequal lengths: four
   // times, so that the long ones are not left alone), of 256 keys at least
-  const int64_t want = (int64_t)num_sms() * kCtasPerSm * (c.batch > 1 ? 4 : 1) / tiles;
+  const int64_t want = (int64_t)num_sms() * ctas_per_sm(rows_tiles(p)) * (c.batch > 1 ? 4 : 1) / tiles;
   int64_t n = want < 1 ? 1 : (want > kMaxSplits ? kMaxSplits : want);
   int64_t chunk = ((max_len + n - 1) / n + 63) & ~int64_t(63);
   if (chunk < 256) chunk = 256;
