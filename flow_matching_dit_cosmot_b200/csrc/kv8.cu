@@ -27,7 +27,7 @@ __device__ __forceinline__ uint32_t cta_max_bf16(uint32_t mag, uint32_t* part) {
 }
 
 template <int kUnits>
-__global__ void __launch_bounds__(kStoreThreads, 3)
+__global__ void __launch_bounds__(kStoreThreads, 4)
     store_kernel(const __grid_constant__ Cache c, const __nv_bfloat16* __restrict__ ksrc,
                  const __nv_bfloat16* __restrict__ vsrc, int64_t ld_src, int64_t src_bstride, int32_t n, int* status) {
   pdl_trigger();
