@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cach
   pdl_trigger();
   pdl_wait();
   __shared__ uint32_t hist[256];
-  __shared__ uint32_t keys[kSelectThreads];
+  __shared__ __align__(16) uint32_t keys[kSelectThreads];
   __shared__ uint32_t sh_prefix, sh_need;
   __shared__ uint32_t warp_cnt[2][kSelectThreads / 32];
   const int32_t b = blockIdx.x / c.n_kv;
@@ -171,9 +171,11 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cach
     keys[tid] = k;
     __syncthreads();
     uint32_t before = 0;
-    for (int i = 0; i < tail - head; ++i) {
-      const uint32_t x = keys[i];
-      before += x > k || (x == k && i < tid) ? 1u : 0u;
+    // keys behind the last free block are 0: below every weight's
+    for (int i = 0; i < tail - head; i += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(keys + i);
+      before += (x.x > k || (x.x == k && i < tid) ? 1u : 0u) + (x.y > k || (x.y == k && i + 1 < tid) ? 1u : 0u) +
+                (x.z > k || (x.z == k && i + 2 < tid) ? 1u : 0u) + (x.w > k || (x.w == k && i + 3 < tid) ? 1u : 0u);
     }
     __syncthreads();
     keys[tid] = mine && before < need ? 1u : 0u;  // block head + tid is among the first `need`
@@ -254,12 +256,13 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cach
 
 // Blocks move towards the front: the source of the j-th kept block is list[j]
 // >= j, ascending.  A thread owns one 16-byte piece of one row of every block
-// and walks j upwards; it reads sources of blocks j and later before it writes
-// block j, and no later source is a block that it has written, so the move is in
-// place without any thread waiting for another.  Two batches of kMoveAhead
-// pieces: one is read while the other is written.  Slice z = 2 moves the scales
-// and the weights in the same order and writes the length.
-constexpr int kMoveAhead = 8, kMoveThreads = 64;
+// and walks j upwards; it has begun to read the sources of block j and of the
+// kMoveRing - 2 after it before it writes block j, and no later source is a
+// block that it has written, so the move is in place without any thread waiting
+// for another.  The pieces wait in the thread's own slots of shared memory.
+// Slice z = 2 moves the scales and the weights in the same order and writes the
+// length.
+constexpr int kMoveAhead = 8, kMoveThreads = 64, kMoveRing = 24;
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ Cache c, const EvictPlan* __restrict__ plan,
                                                          const int32_t* __restrict__ list, const float* weight,
@@ -325,24 +328,31 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   }
   // only the last block may lack the row
   const int32_t end = pl.count - (pl.count > 0 && src[pl.count - 1] * c.block + r >= pl.len ? 1 : 0);
-  uint4 x[2][kMoveAhead];
-  auto read = [&](uint4 (&y)[kMoveAhead], int32_t j) {
-#pragma unroll
-    for (int i = 0; i < kMoveAhead; ++i)
-      if (j + i < end) y[i] = *reinterpret_cast<const uint4*>(base + __ldg(src + j + i) * step);
+  __shared__ __align__(16) uint4 ring[kMoveRing][kMoveThreads];
+  const uint32_t at = smem_u32(&ring[0][threadIdx.x]);
+  auto read = [&](int32_t j, int slot) {
+    if (j < end)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + slot * (kMoveThreads * 16)),
+                   "l"(base + __ldg(src + j) * step)
+                   : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto write = [&](const uint4 (&y)[kMoveAhead], int32_t j) {
 #pragma unroll
-    for (int i = 0; i < kMoveAhead; ++i)
-      if (j + i < end) *reinterpret_cast<uint4*>(base + (j + i) * step) = y[i];
-  };
-  read(x[0], lo);
-  for (int32_t j = lo; j < end; j += 2 * kMoveAhead) {
-    read(x[1], j + kMoveAhead);
-    write(x[0], j);
-    read(x[0], j + 2 * kMoveAhead);
-    write(x[1], j + kMoveAhead);
+  for (int i = 0; i < kMoveRing - 1; ++i) read(lo + i, i);
+  int slot = 0;
+#pragma unroll 4
+  for (int32_t j = lo; j < end; ++j) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kMoveRing - 2) : "memory");
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "r"(at + slot * (kMoveThreads * 16))
+                 : "memory");
+    *reinterpret_cast<uint4*>(base + j * step) = x;
+    read(j + kMoveRing - 1, slot == 0 ? kMoveRing - 1 : slot - 1);
+    slot = slot == kMoveRing - 1 ? 0 : slot + 1;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ host
