@@ -28,8 +28,8 @@ __device__ __forceinline__ uint32_t cta_max_bf16(uint32_t mag, uint32_t* part) {
 
 template <int kUnits>
 __global__ void __launch_bounds__(kStoreThreads, 4)
-    store_kernel(const __grid_constant__ Cache c, const __nv_bfloat16* __restrict__ ksrc,
-                 const __nv_bfloat16* __restrict__ vsrc, int64_t ld_src, int64_t src_bstride, int32_t n, int* status) {
+    store_kernel(const __grid_constant__ Cache c, const __nv_bfloat16* ksrc,
+                 const __nv_bfloat16* vsrc, int64_t ld_src, int64_t src_bstride, int32_t n, int* status) {
   pdl_trigger();
   pdl_wait();
   __shared__ uint32_t part[2][kStoreThreads / 32];
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kStoreThreads, 4)
   for (int u = 0; u < kUnits; ++u) {
     const int32_t row = first + u * step;
     x[u] = make_uint4(0, 0, 0, 0);
-    if (row >= held && row < end) x[u] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(u * step) * ld_src));
+    if (row >= held && row < end) x[u] = load_global(reinterpret_cast<const uint4*>(src + (int64_t)(u * step) * ld_src));
   }
   const float old = row0 < held ? *scale : 0.f;  // read by every thread before thread 0 writes it
   uint32_t mag = 0;
@@ -123,12 +123,13 @@ __global__ void __launch_bounds__(kStoreThreads, 4)
 // stay.  Up to kSelectThreads free blocks every thread counts the blocks that
 // come before its own (one pass over shared memory); above, a radix select over
 // the ordered bits of the weights (four passes of 8 bits) gives the threshold.
-// Then one pass in index order lists the blocks that stay.  The second kernel
-// moves them.
+// Then one pass in index order lists the blocks that stay and moves their scales
+// and weights.  The second kernel moves the rows.
 constexpr int kSelectThreads = 512;
 
-struct EvictPlan {  // per sequence, in the workspace
-  int32_t len, nb, count, reserved;
+struct EvictPlan {  // per sequence and head, in the workspace
+  int32_t len, nb, count;
+  int32_t first;  // the first kept block that moves
 };
 
 // Orders like torch's descending sort: NaN above infinity, both zeros equal.
@@ -138,18 +139,27 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cache c, const float* __restrict__ weight,
-                                                                     int32_t keep, int32_t first_rows,
-                                                                     int32_t last_rows, EvictPlan* plan, int32_t* list,
-                                                                     int* status) {
+__global__ void __launch_bounds__(kSelectThreads)
+    evict_select_kernel(const __grid_constant__ Cache c, const float* weight, int32_t keep, int32_t first_rows,
+                        int32_t last_rows, float* weight_out, EvictPlan* plan, int32_t* list, int* status) {
   pdl_trigger();
   pdl_wait();
   __shared__ uint32_t hist[256];
   __shared__ __align__(16) uint32_t keys[kSelectThreads];
   __shared__ uint32_t sh_prefix, sh_need;
+  __shared__ int32_t sh_first;
   __shared__ uint32_t warp_cnt[2][kSelectThreads / 32];
   const int32_t b = blockIdx.x / c.n_kv;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int64_t base = (int64_t)blockIdx.x * c.n_blocks;
+  const float* w = weight + base;
+  // the first kSelectThreads blocks' values, on their way with the length
+  float w0 = 0.f, ks0 = 0.f, vs0 = 0.f;
+  if (tid < c.n_blocks) {
+    w0 = w[tid];
+    ks0 = c.k_scale[base + tid];
+    vs0 = c.v_scale[base + tid];
+  }
   const int32_t len = shown_rows(c, b, 0, status, tid == 0);
   const int32_t nb = (len + c.block - 1) / c.block;
   // fixed blocks: [0, head) and [tail, nb)
@@ -157,9 +167,8 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cach
   const int32_t tail = max(head, min(nb, (len - min(len, last_rows)) / c.block));
   const int32_t n_fixed = nb - (tail - head);
   const int32_t count = min(nb, max(keep, n_fixed));
-  const float* w = weight + (int64_t)blockIdx.x * c.n_blocks;
-  int32_t* out = list + (int64_t)blockIdx.x * c.n_blocks;
-  if (tid == 0 && blockIdx.x % c.n_kv == 0) plan[b] = EvictPlan{len, nb, count, 0};
+  int32_t* out = list + base;
+  if (tid == 0) sh_first = count;
 
   // threshold: the (count - n_fixed)-th largest key of [head, tail)
   uint32_t prefix = 0, need = (uint32_t)(count - n_fixed);
@@ -167,7 +176,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cach
   const bool count_ranks = !all && need > 0 && tail - head <= kSelectThreads;
   if (count_ranks) {
     const bool mine = tid < tail - head;
-    const uint32_t k = mine ? weight_key(w[head + tid]) : 0u;
+    const uint32_t k = mine ? weight_key(head == 0 ? w0 : w[head + tid]) : 0u;
     keys[tid] = k;
     __syncthreads();
     uint32_t before = 0;
@@ -220,11 +229,17 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cach
   uint32_t kept = 0, ties = 0;
   for (int32_t j0 = 0; j0 < nb; j0 += kSelectThreads) {
     const int32_t j = j0 + tid;
+    // read before anything of this chunk is written (destinations lie at or before their sources)
+    if (j0 > 0 && j < nb) {
+      w0 = w[j];
+      ks0 = c.k_scale[base + j];
+      vs0 = c.v_scale[base + j];
+    }
     bool sure = j < nb && (j < head || j >= tail || all), tie = false;
     if (count_ranks) {
       sure = sure || (j >= head && j < tail && keys[j - head] != 0);
     } else if (j < nb && !sure && count > n_fixed) {
-      const uint32_t k = weight_key(w[j]);
+      const uint32_t k = weight_key(j0 == 0 ? w0 : w[j]);
       sure = k > prefix;
       tie = k == prefix;
     }
@@ -250,8 +265,24 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cach
     }
     kept = total;
     at += __popc(votes & ((1u << lane) - 1u));
-    if (stay && dcheck((int32_t)at < count, status, kWhereKv8Store)) out[at] = j;
+    if (stay && dcheck((int32_t)at < count, status, kWhereKv8Store)) {
+      out[at] = j;
+      if ((int32_t)at < j) {
+        c.k_scale[base + at] = ks0;
+        c.v_scale[base + at] = vs0;
+        atomicMin(&sh_first, (int32_t)at);
+      }
+      weight_out[base + at] = w0;
+    }
   }
+  __syncthreads();
+  for (int32_t j = count + tid; j < c.n_blocks; j += kSelectThreads) {
+    if (j < nb)
+      weight_out[base + j] = 0.f;  // blocks that a later store begins anew
+    else if (weight_out != weight)
+      weight_out[base + j] = w[j];
+  }
+  if (tid == 0) plan[blockIdx.x] = EvictPlan{len, nb, count, sh_first};
 }
 
 // Blocks move towards the front: the source of the j-th kept block is list[j]
@@ -260,56 +291,19 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Cach
 // kMoveRing - 2 after it before it writes block j, and no later source is a
 // block that it has written, so the move is in place without any thread waiting
 // for another.  The pieces wait in the thread's own slots of shared memory.
-// Slice z = 2 moves the scales and the weights in the same order and writes the
-// length.
-constexpr int kMoveAhead = 8, kMoveThreads = 64, kMoveRing = 24;
+constexpr int kMoveThreads = 64, kMoveRing = 24;
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ Cache c, const EvictPlan* __restrict__ plan,
-                                                         const int32_t* __restrict__ list, const float* weight,
-                                                         float* weight_out, int32_t* lens_out, int* status) {
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ Cache c,
+                                                                  const EvictPlan* plan,
+                                                                  const int32_t* list, int32_t* lens_out) {
   pdl_trigger();
   pdl_wait();
   const int32_t b = blockIdx.y / c.n_kv, g = blockIdx.y % c.n_kv;
-  const EvictPlan pl = plan[b];
+  const EvictPlan pl = plan[blockIdx.y];
   const int32_t* src = list + (int64_t)blockIdx.y * c.n_blocks;
-  if (blockIdx.z == 2) {
-    if (blockIdx.x != 0) return;
-    const int64_t base = (int64_t)blockIdx.y * c.n_blocks;
-    // sources lie at or behind their destinations: a chunk is read whole before it is written
-    for (int32_t j0 = 0; j0 < pl.count; j0 += kMoveAhead * kMoveThreads) {
-      float ks[kMoveAhead], vs[kMoveAhead], w[kMoveAhead];
-#pragma unroll
-      for (int i = 0; i < kMoveAhead; ++i) {
-        const int32_t j = j0 + i * kMoveThreads + (int32_t)threadIdx.x;
-        if (j < pl.count) {
-          const int32_t s = src[j];
-          ks[i] = c.k_scale[base + s];
-          vs[i] = c.v_scale[base + s];
-          w[i] = weight[base + s];
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kMoveAhead; ++i) {
-        const int32_t j = j0 + i * kMoveThreads + (int32_t)threadIdx.x;
-        if (j < pl.count && dcheck(j < c.n_blocks, status, kWhereKv8Store)) {
-          c.k_scale[base + j] = ks[i];
-          c.v_scale[base + j] = vs[i];
-          weight_out[base + j] = w[i];
-        }
-      }
-    }
-    __syncthreads();
-    for (int32_t j = pl.count + (int32_t)threadIdx.x; j < c.n_blocks; j += (int32_t)blockDim.x) {
-      if (j < pl.nb)
-        weight_out[base + j] = 0.f;  // blocks that a later store begins anew
-      else if (weight_out != weight)
-        weight_out[base + j] = weight[base + j];
-    }
-    if (g == 0 && threadIdx.x == 0)
-      lens_out[b] = pl.nb == 0 ? 0 : (pl.count - 1) * c.block + (pl.len - (pl.nb - 1) * c.block);
-    return;
-  }
+  const int32_t part = pl.len - (pl.nb - 1) * c.block;  // rows of the last block, which stays if it is not full
+  if (blockIdx.x == 0 && blockIdx.z == 0 && g == 0 && threadIdx.x == 0)
+    lens_out[b] = pl.nb == 0 ? 0 : (pl.count - 1) * c.block + part;
   const int per_row = c.hd >> 4;
   const int unit = (int)blockIdx.x * (int)blockDim.x + (int)threadIdx.x;
   const int32_t r = unit / per_row;
@@ -317,23 +311,13 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   uint8_t* base = (blockIdx.z ? c.v : c.k) + ((int64_t)b * c.bstride + r) * c.ld + (int64_t)g * c.hd +
                   (unit % per_row) * 16;
   const int64_t step = (int64_t)c.block * c.ld;
-  // blocks before the first one that went stay where they are: find it by bisection (list[j] - j never falls)
-  int32_t lo = 0, hi = pl.count;
-  while (lo < hi) {
-    const int32_t mid = (lo + hi) >> 1;
-    if (src[mid] > mid)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  // only the last block may lack the row
-  const int32_t end = pl.count - (pl.count > 0 && src[pl.count - 1] * c.block + r >= pl.len ? 1 : 0);
+  const int32_t lo = pl.first, end = pl.count - (r >= part ? 1 : 0);
   __shared__ __align__(16) uint4 ring[kMoveRing][kMoveThreads];
   const uint32_t at = smem_u32(&ring[0][threadIdx.x]);
   auto read = [&](int32_t j, int slot) {
     if (j < end)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + slot * (kMoveThreads * 16)),
-                   "l"(base + __ldg(src + j) * step)
+                   "l"(base + load_global(src + j) * step)
                    : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -432,7 +416,7 @@ size_t part_bytes(const Cache& c, const Query& p) {
 constexpr int64_t kRowsMax = 32;
 bool use_tiles(const Query& p) { return p.n_rows > kRowsMax; }
 
-size_t evict_list_offset(int32_t batch) { return ((size_t)batch * sizeof(EvictPlan) + 255) & ~size_t(255); }
+size_t evict_list_offset(const Cache& c) { return ((size_t)c.batch * c.n_kv * sizeof(EvictPlan) + 255) & ~size_t(255); }
 
 }  // namespace
 }  // namespace kv8
@@ -545,7 +529,7 @@ extern "C" cosmot_status cosmot_kv8_evict_workspace(const cosmot_kv8_cache* cach
   if (!bytes) return COSMOT_ERR_INVALID_ARG;
   const cosmot_status st = kv8::make_cache(cache, c);
   if (st != COSMOT_OK) return st;
-  *bytes = kv8::evict_list_offset(c.batch) + (size_t)c.batch * c.n_kv * c.n_blocks * sizeof(int32_t);
+  *bytes = kv8::evict_list_offset(c) + (size_t)c.batch * c.n_kv * c.n_blocks * sizeof(int32_t);
   return COSMOT_OK;
 }
 
@@ -563,15 +547,14 @@ extern "C" cosmot_status cosmot_kv8_evict(const cosmot_kv8_cache* cache, const f
   int* status = device_status_ptr();
   if (!status) return COSMOT_ERR_CUDA;
   auto* plan = static_cast<kv8::EvictPlan*>(workspace);
-  auto* list = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kv8::evict_list_offset(c.batch));
+  auto* list = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kv8::evict_list_offset(c));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   st = launch_status(launch_pdl(kv8::evict_select_kernel, dim3((unsigned)(c.batch * c.n_kv)),
                                 dim3(kv8::kSelectThreads), 0, s, nullptr, c, weight, keep_blocks, first_rows, last_rows,
-                                plan, list, status));
+                                weight_out, plan, list, status));
   if (st != COSMOT_OK) return st;
   const unsigned slices = (unsigned)(c.block * c.hd / 16 / kv8::kMoveThreads);  // 64 .. 1024 pieces
-  return launch_status(launch_pdl(kv8::evict_move_kernel, dim3(slices, (unsigned)(c.batch * c.n_kv), 3),
-                                  dim3(kv8::kMoveThreads), 0, s,
-                                  nullptr, c, (const kv8::EvictPlan*)plan, (const int32_t*)list, weight, weight_out,
-                                  lens_out, status));
+  return launch_status(launch_pdl(kv8::evict_move_kernel, dim3(slices, (unsigned)(c.batch * c.n_kv), 2),
+                                  dim3(kv8::kMoveThreads), 0, s, nullptr, c, (const kv8::EvictPlan*)plan,
+                                  (const int32_t*)list, lens_out));
 }

@@ -86,8 +86,8 @@ __device__ __forceinline__ float load_q_row(const __nv_bfloat16* row, bool valid
     for (int i = 0; i < 8; ++i) w[h][i] = 0;
     if (valid) {
       const uint4* p = reinterpret_cast<const uint4*>(row + 64 * h + 16 * j);
-      *reinterpret_cast<uint4*>(&w[h][0]) = __ldg(p);
-      *reinterpret_cast<uint4*>(&w[h][4]) = __ldg(p + 1);
+      *reinterpret_cast<uint4*>(&w[h][0]) = load_global(p);
+      *reinterpret_cast<uint4*>(&w[h][4]) = load_global(p + 1);
     }
   }
 #pragma unroll
@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
   for (int i = 0; i < kRing - 1; ++i) fetch(first + i * kStep, i);
   auto scale_of = [&](int32_t blk) {
     float4 s;
-    s.x = __ldg(ksp + blk);
-    scale_log2_parts(__ldg(vsp + blk), s.y, s.z);
+    s.x = load_global(ksp + blk);
+    scale_log2_parts(load_global(vsp + blk), s.y, s.z);
     s.w = 0.f;
     return s;
   };
@@ -511,7 +511,7 @@ struct WeighRing {
 template <int HD, int NT>
 __global__ void __launch_bounds__(32 * kWarps) rows_weigh_kernel(const __grid_constant__ Cache c,
                                                                 const __grid_constant__ Query p, float decay,
-                                                                float* __restrict__ weight) {
+                                                                float* weight) {
   pdl_trigger();
   pdl_wait();
   using R = WeighRing<HD>;
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(32 * kWarps) rows_weigh_kernel(const __grid_co
     lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 2));
     float sum = 0.f, ks = 0.f, before = 0.f;
     // a block's scale and old weight are loaded one block ahead
-    float ks_next = __ldg(ksp + blk0), before_next = wp[blk0];
+    float ks_next = load_global(ksp + blk0), before_next = wp[blk0];
     int slot = 0;
 #pragma unroll 1
     for (int t = 0; t < n; ++t) {
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(32 * kWarps) rows_weigh_kernel(const __grid_co
         before = before_next;
         const int32_t ahead = blk0 + ((t >> shift) + 1) * kWarps;
         if (ahead < blk1) {
-          ks_next = __ldg(ksp + ahead);
+          ks_next = load_global(ksp + ahead);
           before_next = wp[ahead];
         }
       }

@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int i = 0; i < kLoads; ++i) {
         const int r = row + i * kConvWarps * kRows;
         w[i] = make_uint4(0, 0, 0, 0);
-        if (r < kTile && kt * kTile + r < kend) w[i] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)(kt * kTile + r) * c.ld));
+        if (r < kTile && kt * kTile + r < kend) w[i] = load_global(reinterpret_cast<const uint4*>(base + (int64_t)(kt * kTile + r) * c.ld));
       }
     };
     auto widen = [&](const uint4 (&w)[kLoads], int slot) {
@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       float4 sc = make_float4(1.f, 0.f, 0.f, 0.f);  // a group behind the end: finite, and every key masked
       if (cw == 0 && lane < NG && kt * kTile + lane * kGroupKeys < kend) {
         const int64_t at = (int64_t)bg * c.n_blocks + kt * NG + lane;
-        sc.x = __ldg(c.k_scale + at);
-        scale_log2_parts(__ldg(c.v_scale + at), sc.y, sc.z);
+        sc.x = load_global(c.k_scale + at);
+        scale_log2_parts(load_global(c.v_scale + at), sc.y, sc.z);
       }
       if (!empty(2 * j)) break;
       widen(wk, (2 * j) % kSlots);
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int64_t from = __shfl_sync(0xffffffffu, at, row);
         const bool live = __shfl_sync(0xffffffffu, (int)valid, row) != 0;
         x[i] = make_uint4(0, 0, 0, 0);
-        if (live) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + from) + piece);
+        if (live) x[i] = load_global(reinterpret_cast<const uint4*>(p.q + from) + piece);
       }
       {
 #pragma unroll
@@ -641,7 +641,7 @@ __device__ __forceinline__ WeighItem weigh_item(const Cache& c, const Query& p, 
 template <int HD>
 __global__ void __launch_bounds__(kWeighThreads, 1)
     tile_weigh_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ Cache c,
-                      const __grid_constant__ Query p, float decay, float* __restrict__ weight, int32_t q_tile,
+                      const __grid_constant__ Query p, float decay, float* weight, int32_t q_tile,
                       int32_t ranges) {
   using C = WeighCfg<HD>;
   extern __shared__ uint8_t smem_raw[];
@@ -830,7 +830,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
           for (int i = 0; i < kAhead; ++i) {
             const int row = r0 + 2 * kRows * i;
             x[i] = make_uint4(0, 0, 0, 0);
-            if (w.k0 + row < w.k_end) x[i] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(w.k0 + row) * c.ld));
+            if (w.k0 + row < w.k_end) x[i] = load_global(reinterpret_cast<const uint4*>(src + (int64_t)(w.k0 + row) * c.ld));
           }
 #pragma unroll
           for (int i = 0; i < kAhead; ++i) {
@@ -886,14 +886,14 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       for (int g = 0; g < 8; ++g) {
         acc[g] = 0.f;
         const int32_t key = kbase + 16 * g;
-        f[g] = key < w.k_end ? p.scale_log2 * __ldg(c.k_scale + (int64_t)w.bg * c.n_blocks + key / c.block) : 0.f;
+        f[g] = key < w.k_end ? p.scale_log2 * load_global(c.k_scale + (int64_t)w.bg * c.n_blocks + key / c.block) : 0.f;
       }
       const float* lse_row = p.lse + ((int64_t)w.b * p.n_heads + (w.bg % c.n_kv) * p.group + hr) * p.n_q;
       {
         // rows that are not there weigh 2^-inf; a tile's lse is loaded one tile ahead
         auto load_lse = [&](int i) {
           const int64_t qi = (int64_t)(w.i0 + i) * q_tile + qr;
-          return row < tile_rows && qi < p.n_q ? __ldg(lse_row + qi) : INFINITY;
+          return row < tile_rows && qi < p.n_q ? load_global(lse_row + qi) : INFINITY;
         };
         const int first = (phase ^ n) & 1;
         float ls_next = first < w.n_i ? load_lse(first) : 0.f;

@@ -352,6 +352,23 @@ def test_evict_in_place_is_the_same():
     assert torch.equal(cs[0].k_scale.nan_to_num(), cs[1].k_scale.nan_to_num())
 
 
+def test_evict_again_and_again_is_the_same():
+    """The moves start while the selection before them still runs: they must wait for what it writes."""
+    lens = [300, 211]
+    ref = None
+    for k in range(40):
+        c = filled(2, 320, 1, 128, 64, lens, seed=44)
+        w = torch.rand((2, 1, c.n_blocks), generator=torch.Generator("cuda").manual_seed(7), device="cuda")
+        junk = torch.full((1 << 16,), 0xc0 + k % 8, dtype=torch.uint8, device="cuda")  # what the workspace may hold before
+        del junk
+        c.evict(w, 3)
+        got = (c.lens, w, c.k_scale.nan_to_num(), c.k.view(torch.uint8), c.v.view(torch.uint8))
+        if ref is None:
+            ref = got
+        for a, b in zip(ref, got):
+            assert torch.equal(a, b)
+
+
 def test_evict_many_blocks():
     """More blocks than a CTA's threads, most of them equal."""
     lens = [60_000]
