@@ -55,6 +55,12 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // 32 bytes to a 32-byte-aligned address.
 __device__ __forceinline__ void st_global32(void* dst, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
@@ -83,8 +89,7 @@ template <int HD>
 struct AttnCfg {
   static constexpr int kTileBytes = kTile * HD * 2;
   static constexpr int kScaleBytes = 4 * 8 * 16;  // four key tiles in flight, eight groups each
-  static constexpr int kFacBytes = 2 * kTile * 4;  // the query rows' factors
-  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 256 + kScaleBytes + kFacBytes + 1024;
+  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 256 + kScaleBytes + 1024;
   static constexpr uint32_t kIdescS = idesc_f16_f32(kTile, kTile, false);
   static constexpr uint32_t kIdescO = idesc_f16_f32(kTile, HD, true);
   __device__ static constexpr uint32_t s_col(int t) { return (uint32_t)t * 128u; }
@@ -112,7 +117,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 1 + 2 * kSlots + 7);
   // [4][NG] (ks, log2 vs, 1/vs)
   float4* scales = reinterpret_cast<float4*>(smem + (2 + kSlots) * C::kTileBytes + 256);
-  float* facs = reinterpret_cast<float*>(smem + (2 + kSlots) * C::kTileBytes + 256 + C::kScaleBytes);
   constexpr int kGroupKeys = kTile / NG;
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
@@ -305,52 +309,55 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const bool valid = r < p.n_rows;
     const int32_t qi = valid ? (int32_t)((uint32_t)r / (uint32_t)p.group) : 0;
     const int32_t h = kvh * p.group + (valid ? (int32_t)r - qi * p.group : 0);
-    // Q: a warp's 32 rows, 16 bytes a lane, several whole rows at a time
+    // Q: a warp's 32 rows come into their places as bf16, whole rows at a time;
+    // then every lane turns its own row into f16 where it lies.  Short loops: a
+    // CTA runs this once, and code that was never run comes in slowly.
+    float fac = p.scale_log2;
     if (n_vis > 0 && (t == 0 || two)) {
-      constexpr int kLanes = HD / 8, kRows = 32 / kLanes;  // lanes of a row, rows of one load
+      constexpr int kLanes = HD / 8, kRows = 32 / kLanes;  // lanes of a row, rows of one copy
       const int64_t at = (int64_t)(b * p.q_bstride + qi) * p.ld_q + (int64_t)h * HD;  // this lane's own row
-      const uint32_t dst = sQ + t * C::kTileBytes;
+      const uint32_t tile = sQ + t * C::kTileBytes;
       const int piece = lane % kLanes;
-      uint4 x[32 / kRows];
-#pragma unroll
+#pragma unroll 2
       for (int i = 0; i < 32 / kRows; ++i) {
         const int row = i * kRows + lane / kLanes;
         const int64_t from = __shfl_sync(0xffffffffu, at, row);
-        const bool live = __shfl_sync(0xffffffffu, (int)valid, row) != 0;
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (live) x[i] = load_global(reinterpret_cast<const uint4*>(p.q + from) + piece);
+        const int live = __shfl_sync(0xffffffffu, (int)valid, row) ? 16 : 0;  // 0: zeros
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + sw_offset(lane_base + row, piece)),
+                     "l"(p.q + from + piece * 8), "r"(live)
+                     : "memory");
       }
-      {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      uint32_t mag = 0;  // magnitudes of bf16 order like their bits
+#pragma unroll 4
+      for (int i = 0; i < kLanes; ++i) {
+        const uint4 x = ld_shared16(tile + sw_offset(lane_base + lane, i));
+        mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+      }
+      mag = max(mag & 0xffffu, mag >> 16);
+      // below 2^-47 a row loses bits of less than 2^-85: nothing that a key could raise to a visible score
+      int e2 = (int)(mag >> 7) - 127 - 13;
+      e2 = e2 < -60 ? -60 : (e2 > 114 ? 114 : e2);
+      const float down = exp2_int(-e2);
+      fac = mag < 0x7f80u ? fmaxf(p.scale_log2 * exp2_int(e2), 1e-25f) : __int_as_float(0x7fc00000);
+#pragma unroll 2
+      for (int i = 0; i < kLanes; ++i) {
+        const uint32_t where = tile + sw_offset(lane_base + lane, i);
+        const uint4 x = ld_shared16(where);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
+        uint32_t y[4];
 #pragma unroll
-        for (int i = 0; i < 32 / kRows; ++i) {
-          const int row = i * kRows + lane / kLanes;
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i]);
-          // magnitudes of bf16 order like their bits
-          uint32_t mag = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-#pragma unroll
-          for (int off = 1; off < kLanes; off <<= 1) mag = __vmaxu2(mag, __shfl_xor_sync(0xffffffffu, mag, off));
-          mag = max(mag & 0xffffu, mag >> 16);
-          // below 2^-47 a row loses bits of less than 2^-85: nothing that a key could raise to a visible score
-          int e2 = (int)(mag >> 7) - 127 - 13;
-          e2 = e2 < -60 ? -60 : (e2 > 114 ? 114 : e2);
-          const float down = exp2_int(-e2);
-          if (piece == 0)
-            facs[t * kTile + lane_base + row] =
-                mag < 0x7f80u ? fmaxf(p.scale_log2 * exp2_int(e2), 1e-25f) : __int_as_float(0x7fc00000);
-          uint32_t y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 v = unpack_bf16x2(w[e]);
-            y[e] = pack_f16x2(v.x * down, v.y * down);
-          }
-          st_shared16(dst + sw_offset(lane_base + row, piece), y[0], y[1], y[2], y[3]);
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = unpack_bf16x2(w[e]);
+          y[e] = pack_f16x2(v.x * down, v.y * down);
         }
+        st_shared16(where, y[0], y[1], y[2], y[3]);
       }
       fence_proxy_async_smem();
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_q);
-    const float fac = facs[t * kTile + lane_base + lane];
 
     const uint32_t s_addr = tmem_base + ((uint32_t)lane_base << 16) + C::s_col(t);
     const uint32_t o_addr = tmem_base + ((uint32_t)lane_base << 16) + C::o_col(t);
