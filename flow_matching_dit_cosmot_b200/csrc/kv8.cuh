@@ -120,49 +120,10 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ void store_o8(__nv_bfloat16* dst, const float* v) {
-  uint4 x;
-  x.x = pack_bf16x2(v[0], v[1]);
-  x.y = pack_bf16x2(v[2], v[3]);
-  x.z = pack_bf16x2(v[4], v[5]);
-  x.w = pack_bf16x2(v[6], v[7]);
-  *reinterpret_cast<uint4*>(dst) = x;
-}
-
 // Key splits of a row: split s gives o_s = sum 2^(x - ref_s) v8 and (ref_s,
 // l_s) with l_s = sum 2^(x - ref_s) / vs; where a split shows the row nothing,
-// l_s = 0 and o_s is not read.  Joins 8 columns of packed row pr, in split order.
-template <int HD>
-__device__ __forceinline__ void join_row(const float* part_o, const float2* part_ml, int splits, int64_t rows, int64_t pr,
-                                         int col, float (&acc)[8], float& lse) {
-  float ref = -INFINITY, l = 0.f;
-  for (int s = 0; s < splits; ++s) {
-    const float2 ml = part_ml[s * rows + pr];
-    if (ml.y != 0.f) ref = fmaxf(ref, ml.x);
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  for (int s = 0; s < splits; ++s) {
-    const float2 ml = part_ml[s * rows + pr];
-    if (ml.y == 0.f) continue;
-    const float f = ex2_approx(ml.x - ref);
-    l = fmaf(f, ml.y, l);
-    const float4* src = reinterpret_cast<const float4*>(part_o + (s * rows + pr) * HD + col);
-    const float4 x = src[0], y = src[1];
-    acc[0] = fmaf(f, x.x, acc[0]);
-    acc[1] = fmaf(f, x.y, acc[1]);
-    acc[2] = fmaf(f, x.z, acc[2]);
-    acc[3] = fmaf(f, x.w, acc[3]);
-    acc[4] = fmaf(f, y.x, acc[4]);
-    acc[5] = fmaf(f, y.y, acc[5]);
-    acc[6] = fmaf(f, y.z, acc[6]);
-    acc[7] = fmaf(f, y.w, acc[7]);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] *= inv;
-  lse = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
-}
+// l_s = 0 and o_s is zero or was not written (each kernel says which).
+constexpr int kMaxSplits = 256;
 
 // Checked host-side views of the public structs.
 cosmot_status make_cache(const cosmot_kv8_cache* c, Cache& out);

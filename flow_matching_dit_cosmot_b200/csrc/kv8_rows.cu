@@ -418,27 +418,30 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
   }
 }
 
-// Joins the key ranges of one row a CTA: 128 threads are 32 x 4 columns (hd 64:
-// 16 x 4) by groups that take the ranges in turn; the groups' sums are added in
-// order.
-constexpr int kMaxSplits = 256;
+constexpr int kJoinThreads = 128;
 
+// One row a CTA: its threads are hd / 4 columns of 4 by groups that take the
+// splits in turn; the groups' sums are added in order.  (A split without a key
+// for the row may have written nothing: it is not read.)
 template <int HD>
-__global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ Cache c, const __grid_constant__ Query p) {
+__global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const __grid_constant__ Cache c,
+                                                                 const __grid_constant__ Query p) {
   pdl_trigger();
   pdl_wait();
-  constexpr int kCols = HD / 4, kGroups = 128 / kCols;
+  const int64_t stride = (int64_t)c.batch * c.n_kv * p.n_rows, pr = blockIdx.x, r = pr % p.n_rows, bg = pr / p.n_rows;
+  const int32_t b = (int32_t)(bg / c.n_kv), kvh = (int32_t)(bg % c.n_kv);
+  const int splits = p.splits;
+  constexpr int kCols = HD / 4, kGroups = kJoinThreads / kCols;
   __shared__ float wgt[kMaxSplits];
   __shared__ float red[2][4];
   __shared__ float4 part[kGroups][kCols];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t rows = (int64_t)c.batch * c.n_kv * p.n_rows, pr = blockIdx.x;
-  float2 ml[kMaxSplits / 128];
+  float2 ml[kMaxSplits / kJoinThreads];
   float ref = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kMaxSplits / 128; ++i) {
-    const int s = tid + 128 * i;
-    ml[i] = s < p.splits ? p.part_ml[s * rows + pr] : make_float2(-INFINITY, 0.f);
+  for (int i = 0; i < kMaxSplits / kJoinThreads; ++i) {
+    const int s = tid + kJoinThreads * i;
+    ml[i] = s < splits ? p.part_ml[s * stride + pr] : make_float2(-INFINITY, 0.f);
     if (ml[i].y != 0.f) ref = fmaxf(ref, ml[i].x);
   }
 #pragma unroll
@@ -448,9 +451,9 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
   ref = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
   float lsum = 0.f;
 #pragma unroll
-  for (int i = 0; i < kMaxSplits / 128; ++i) {
+  for (int i = 0; i < kMaxSplits / kJoinThreads; ++i) {
     const float f = ml[i].y == 0.f ? 0.f : ex2_approx(ml[i].x - ref);
-    wgt[tid + 128 * i] = f;
+    wgt[tid + kJoinThreads * i] = f;
     lsum = fmaf(f, ml[i].y, lsum);
   }
 #pragma unroll
@@ -462,10 +465,10 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const float* src = p.part_o + pr * HD + col * 4;
 #pragma unroll 8
-  for (int s = grp; s < p.splits; s += kGroups) {
+  for (int s = grp; s < splits; s += kGroups) {
     const float f = wgt[s];
-    if (f != 0.f) {  // a range that shows the row nothing wrote nothing
-      const float4 x = *reinterpret_cast<const float4*>(src + (int64_t)s * rows * HD);
+    if (f != 0.f) {
+      const float4 x = *reinterpret_cast<const float4*>(src + (int64_t)s * stride * HD);
       acc.x = fmaf(f, x.x, acc.x);
       acc.y = fmaf(f, x.y, acc.y);
       acc.z = fmaf(f, x.z, acc.z);
@@ -484,8 +487,6 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
     acc.w += x.w;
   }
   const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-  const int64_t bg = pr / p.n_rows, r = pr % p.n_rows;
-  const int32_t b = (int32_t)(bg / c.n_kv), kvh = (int32_t)(bg % c.n_kv);
   const int64_t qi = r / p.group;
   const int32_t h = kvh * p.group + (int32_t)(r % p.group);
   if (!dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store)) return;
@@ -667,8 +668,8 @@ cosmot_status rows_attention(const Cache& c, const Query& p, cudaStream_t s) {
     st = one ? launch_attention<64, 1>(c, p, s) : launch_attention<64, 2>(c, p, s);
   if (st != COSMOT_OK || p.splits == 1) return st;
   const dim3 jgrid((unsigned)((int64_t)c.batch * c.n_kv * p.n_rows));
-  return launch_status(c.hd == 128 ? launch_pdl(rows_join_kernel<128>, jgrid, dim3(128), 0, s, nullptr, c, p)
-                                   : launch_pdl(rows_join_kernel<64>, jgrid, dim3(128), 0, s, nullptr, c, p));
+  return launch_status(c.hd == 128 ? launch_pdl(rows_join_kernel<128>, jgrid, dim3(kJoinThreads), 0, s, nullptr, c, p)
+                                   : launch_pdl(rows_join_kernel<64>, jgrid, dim3(kJoinThreads), 0, s, nullptr, c, p));
 }
 
 cosmot_status rows_weigh(const Cache& c, const Query& p0, float decay, float* weight, int32_t max_len, cudaStream_t s) {

@@ -81,8 +81,11 @@ constexpr int kConvWarps = 7;
 struct TilePlan {
   int32_t pairs;    // pairs of query tiles of a (sequence, key head)
   int32_t n_full;   // leading items that one CTA takes whole
-  int32_t n_tail;   // the others, `splits` CTAs each
+  int32_t n_lo;     // the next ones, `splits` CTAs each
+  int32_t n_hi;     // the last ones, splits + 1 CTAs each
   int32_t splits;
+  // CTAs behind the whole items; each writes 2 * kTile rows of partial results
+  __host__ __device__ int32_t n_parts() const { return n_lo * splits + n_hi * (splits + 1); }
 };
 
 template <int HD>
@@ -122,10 +125,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
   // work item: the pairs of all heads in turn (causal: the longest first)
   int32_t item = (int32_t)blockIdx.x, split = 0, splits = 1;
-  if (item >= plan.n_full) {
-    split = (item - plan.n_full) % plan.splits;
-    item = plan.n_full + (item - plan.n_full) / plan.splits;
-    splits = plan.splits;
+  const int32_t slot_of_part = item - plan.n_full;
+  if (slot_of_part >= 0) {
+    const int32_t lo = plan.n_lo * plan.splits;
+    splits = slot_of_part < lo ? plan.splits : plan.splits + 1;
+    const int32_t t = slot_of_part < lo ? slot_of_part : slot_of_part - lo;
+    split = t % splits;
+    item = plan.n_full + (slot_of_part < lo ? 0 : plan.n_lo) + t / splits;
   }
   const int32_t heads = c.batch * c.n_kv;
   const int32_t bg = item % heads, b = bg / c.n_kv, kvh = bg % c.n_kv;
@@ -477,7 +483,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       const bool store = valid && dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store);
       const bool none = l == 0.f;  // the row saw nothing here
-      const int64_t pr = ((int64_t)split * plan.n_tail + (item - plan.n_full)) * 2 * kTile + t * kTile + lane_base + lane;
+      const int64_t pr = (int64_t)slot_of_part * 2 * kTile + t * kTile + lane_base + lane;
       const float inv = splits > 1 ? 1.f : 1.f / l;
       if (store && ok) {
         if (splits > 1)
@@ -525,29 +531,59 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (warp == 0) tmem_dealloc(tmem_base, 512);
 }
 
-// Joins the key splits of the tail items' rows, in split order; a thread has 8 columns.
+// Joins the key splits, in their order: hd / 4 lanes a row of a split item, 4
+// columns each.  (The few-row join's CTA a row took 23 us where this takes 11,
+// for 76 items of three or four splits.)
+constexpr int kTileJoinThreads = 256;
+
 template <int HD>
-__global__ void __launch_bounds__(256) tile_join_kernel(const __grid_constant__ Cache c, const __grid_constant__ Query p,
-                                                        const __grid_constant__ TilePlan plan) {
+__global__ void __launch_bounds__(kTileJoinThreads) tile_join_kernel(const __grid_constant__ Cache c,
+                                                                     const __grid_constant__ Query p,
+                                                                     const __grid_constant__ TilePlan plan) {
   pdl_trigger();
   pdl_wait();
-  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t rows = (int64_t)plan.n_tail * 2 * kTile;
-  if (u >= rows * (HD / 8)) return;
-  const int64_t pr = u / (HD / 8);
-  const int col = (int)(u % (HD / 8)) * 8;
-  const int32_t heads = c.batch * c.n_kv, item = plan.n_full + (int32_t)(pr / (2 * kTile));
-  const int32_t bg = item % heads, b = bg / c.n_kv, kvh = bg % c.n_kv;
+  constexpr int kLanes = HD / 4, kRowsOfCta = kTileJoinThreads / kLanes;
+  constexpr int kCtas = 2 * kTile / kRowsOfCta;  // of an item
+  const int32_t i = (int32_t)(blockIdx.x / kCtas);
+  const int32_t row = (int32_t)(blockIdx.x % kCtas) * kRowsOfCta + (int32_t)threadIdx.x / kLanes;
+  const bool lo = i < plan.n_lo;
+  const int splits = lo ? plan.splits : plan.splits + 1;
+  const int64_t part = lo ? (int64_t)i * plan.splits
+                          : (int64_t)plan.n_lo * plan.splits + (int64_t)(i - plan.n_lo) * (plan.splits + 1);
+  const int32_t heads = c.batch * c.n_kv, item = plan.n_full + i, bg = item % heads, b = bg / c.n_kv, kvh = bg % c.n_kv;
   const int32_t pair = p.causal ? plan.pairs - 1 - item / heads : item / heads;
-  const int64_t r = (int64_t)pair * 2 * kTile + pr % (2 * kTile);
+  const int64_t r = (int64_t)pair * 2 * kTile + row;
   if (r >= p.n_rows) return;
-  float acc[8], lse;
-  join_row<HD>(p.part_o, p.part_ml, plan.splits, rows, pr, col, acc, lse);
-  const int64_t qi = r / p.group;
-  const int32_t h = kvh * p.group + (int32_t)(r % p.group);
+  const int64_t pr = part * 2 * kTile + row;
+  const int col = ((int)threadIdx.x % kLanes) * 4;
+  const float2* ml = p.part_ml + pr;
+  float ref = -INFINITY;
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float2 x = ml[(int64_t)s * 2 * kTile];
+    if (x.y != 0.f) ref = fmaxf(ref, x.x);
+  }
+  float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const float* src = p.part_o + pr * HD + col;
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float2 m = ml[(int64_t)s * 2 * kTile];
+    // (a range that shows the row nothing wrote zeros)
+    const float4 x = *reinterpret_cast<const float4*>(src + (int64_t)s * 2 * kTile * HD);
+    const float f = m.y == 0.f ? 0.f : ex2_approx(m.x - ref);
+    l = fmaf(f, m.y, l);
+    acc[0] = fmaf(f, x.x, acc[0]);
+    acc[1] = fmaf(f, x.y, acc[1]);
+    acc[2] = fmaf(f, x.z, acc[2]);
+    acc[3] = fmaf(f, x.w, acc[3]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int32_t qi = (int32_t)((uint32_t)r / (uint32_t)p.group), h = kvh * p.group + (int32_t)r - qi * p.group;
   if (!dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store)) return;
-  store_o8(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col, acc);
-  if (col == 0 && p.lse) p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = lse;
+  *reinterpret_cast<uint2*>(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col) =
+      make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  if (col == 0 && p.lse)
+    p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------ weighing
@@ -1000,17 +1036,24 @@ TilePlan make_plan(const Cache& c, const Query& p, int32_t max_len) {
   const int64_t n_kt = ((int64_t)max_len + kTile - 1) / kTile;
   t.splits = 1;
   t.n_full = (int32_t)items;
-  // Items of a last wave that does not fill the SMs are split over the keys, the
-  // way that takes the fewest key tiles in turn; a CTA's start and end cost it
-  // about four more, and joining a split about one for every 64 items.
+  // Items of a last wave that does not fill the SMs are split over the keys into
+  // m full waves of CTAs, so that m (the longest range + a start and an end, about
+  // four key tiles) and the join, about one for every 48 CTAs, take the least.
   const int64_t tail = items % sms;
   double best = (double)(n_kt + 4);
-  for (int64_t k = 2; tail > 0 && k <= 32 && 2 * k <= n_kt; ++k) {
-    const double cost = (double)((tail * k + sms - 1) / sms) * ((double)((n_kt + k - 1) / k) + 4) + (double)(tail * k) / 64 + 2;
+  for (int64_t m = 1; tail > 0 && m <= 6; ++m) {
+    int64_t k = m * sms / tail, hi = m * sms - k * tail;  // hi items take one range more
+    if (k > kMaxSplits - 1) k = kMaxSplits - 1;
+    if (2 * k > n_kt) k = n_kt / 2;  // two key tiles a range at least
+    if (k != m * sms / tail || 2 * (k + 1) > n_kt) hi = 0;
+    if (k < 1 || (k == 1 && hi < tail)) continue;
+    const double first = (double)((n_kt + k - 1) / k), rest = (double)((n_kt + (hi > 0 ? k : k - 1)) / (hi > 0 ? k + 1 : k));
+    const double cost = first + (double)(m - 1) * rest + 4.0 * (double)m + (double)(tail * k + hi) / 48 + 2;
     if (cost < best) {
       best = cost;
       t.splits = (int32_t)k;
-      t.n_tail = (int32_t)tail;
+      t.n_lo = (int32_t)(tail - hi);
+      t.n_hi = (int32_t)hi;
       t.n_full = (int32_t)(items - tail);
     }
   }
@@ -1018,7 +1061,7 @@ TilePlan make_plan(const Cache& c, const Query& p, int32_t max_len) {
 }
 
 size_t plan_o_bytes(const TilePlan& t, int hd) {
-  return ((size_t)t.splits * t.n_tail * 2 * kTile * hd * 4 + 255) & ~size_t(255);
+  return ((size_t)t.n_parts() * 2 * kTile * hd * 4 + 255) & ~size_t(255);
 }
 
 // Sets a kernel's shared-memory limit once per device; `regs` is the sum that
@@ -1044,7 +1087,7 @@ cosmot_status launch_tiles(const Cache& c, const Query& p, const TilePlan& t, cu
   const cosmot_status st = prepare(tile_attention_kernel<HD, NG>, AttnCfg<HD>::kSmem, 256 * (kRegsIo + kRegsSoftmax),
                                    kAttnThreads, done);
   if (st != COSMOT_OK) return st;
-  const int64_t grid = t.n_full + (int64_t)t.n_tail * t.splits;
+  const int64_t grid = (int64_t)t.n_full + t.n_parts();
   return launch_status(launch_pdl(tile_attention_kernel<HD, NG>, dim3((unsigned)grid), dim3(kAttnThreads),
                                   AttnCfg<HD>::kSmem, s, nullptr, c, p, t));
 }
@@ -1055,9 +1098,9 @@ cosmot_status launch_attention(const Cache& c, const Query& p, const TilePlan& t
                            : c.block == 64 ? launch_tiles<HD, 2>(c, p, t, s)
                            : c.block == 32 ? launch_tiles<HD, 4>(c, p, t, s)
                                            : launch_tiles<HD, 8>(c, p, t, s);
-  if (st != COSMOT_OK || t.n_tail == 0) return st;
-  const int64_t units = (int64_t)t.n_tail * 2 * kTile * (HD / 8);
-  return launch_status(launch_pdl(tile_join_kernel<HD>, dim3((unsigned)((units + 255) / 256)), dim3(256), 0, s, nullptr, c,
+  if (st != COSMOT_OK || t.n_parts() == 0) return st;
+  return launch_status(launch_pdl(tile_join_kernel<HD>, dim3((unsigned)(t.n_lo + t.n_hi) * (unsigned)(2 * kTile * (HD / 4) / kTileJoinThreads)),
+                                  dim3(kTileJoinThreads), 0, s, nullptr, c,
                                   p, t));
 }
 
@@ -1092,14 +1135,14 @@ cosmot_status launch_weigh(const Cache& c, const Query& p, float decay, float* w
 
 size_t tile_workspace(const Cache& c, const Query& p, int32_t max_len) {
   const TilePlan t = make_plan(c, p, max_len);
-  return t.n_tail == 0 ? 0 : plan_o_bytes(t, c.hd) + (size_t)t.splits * t.n_tail * 2 * kTile * sizeof(float2);
+  return t.n_parts() == 0 ? 0 : plan_o_bytes(t, c.hd) + (size_t)t.n_parts() * 2 * kTile * sizeof(float2);
 }
 
 cosmot_status tile_attention(const Cache& c, const Query& p0, int32_t max_len, void* workspace, cudaStream_t s) {
   Query p = p0;
   const TilePlan t = make_plan(c, p, max_len);
   if ((int64_t)c.batch * c.n_kv * t.pairs > INT32_MAX / 64) return COSMOT_ERR_UNSUPPORTED;
-  if (t.n_tail) {
+  if (t.n_parts()) {
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan_o_bytes(t, c.hd));
   }
