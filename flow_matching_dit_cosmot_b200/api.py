@@ -327,7 +327,7 @@ class KVCache8:
                                capacity, n_kv, hd, block, 0)
         self._ref = ctypes.byref(self.desc)
         self._plans = {}
-        self._evict_bytes = None
+        self._evict_like = None
 
     @classmethod
     def empty(cls, batch: int, capacity: int, n_kv_heads: int, head_dim: int, block: int = 64, device="cuda"):
@@ -377,33 +377,41 @@ class KVCache8:
         if code != L.COSMOT_OK:
             raise L.CosmotError(name, code)
 
-    def _workspace(self, need: int, workspace: Optional[torch.Tensor]):
+    def _shape(self, shape, dtype):
+        """One element seen as a tensor of `shape`: torch.empty_like gives a new contiguous one."""
+        return torch.empty((1,), dtype=dtype, device=self.device).expand(shape)
+
+    def _workspace(self, need: int, like: Optional[torch.Tensor], workspace: Optional[torch.Tensor]):
         """(tensor, made here): the caller's workspace, or one for this call."""
         if workspace is not None:
             self._here("workspace", workspace)
             if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
                 raise ValueError(f"workspace: expected at least {need} contiguous uint8 elements")
             return workspace, None
-        made = self.k_scale.new_empty((need,), dtype=torch.uint8) if need else None
+        made = torch.empty_like(like, memory_format=torch.contiguous_format) if need else None
         return made, made
 
     def _query(self, q: torch.Tensor, n_new: int, causal: bool, max_len: int, softmax_scale: float, o_between: int = 0):
-        """(descriptor, attention's workspace bytes, elements between q's rows).  The
-        first two depend on sizes alone and are kept for calls of the same sizes."""
-        ld, between = _rows_layout(q, "q", self.batch, None, self.head_dim, torch.bfloat16)
-        self._here("q", q)
-        n, heads = q.shape[1], q.shape[2]
-        key = (n, heads, between, o_between, n_new, causal, max_len, softmax_scale)
+        """(descriptor, elements between q's rows, attention's workspace bytes, and the
+        shapes of o, lse and the workspace).  They depend on sizes and strides alone and
+        are kept for calls of the same ones."""
+        key = (q.shape, q.stride(), q.dtype, o_between, n_new, causal, max_len, softmax_scale)
         plan = self._plans.get(key)
         if plan is None:
+            ld, between = _rows_layout(q, "q", self.batch, None, self.head_dim, torch.bfloat16)
+            self._here("q", q)
+            _, n, heads, hd = q.shape
             desc = L.Kv8Query(n, between, o_between or n, heads, n_new, L.COSMOT_KV8_CAUSAL if causal else L.COSMOT_KV8_FULL,
                               max_len, softmax_scale, 0)
             need = ctypes.c_size_t(0)
             self._call("cosmot_kv8_attention_workspace", ctypes.byref(desc), ctypes.byref(need))
             if len(self._plans) >= 64:
                 self._plans = {}
-            plan = self._plans[key] = (ctypes.byref(desc), need.value)
-        return plan[0], plan[1], ld
+            plan = self._plans[key] = (ctypes.byref(desc), ld, need.value, self._shape(q.shape, torch.bfloat16),
+                                       self._shape((self.batch, heads, n), torch.float32),
+                                       self._shape((need.value,), torch.uint8))
+        self._here("q", q)
+        return plan
 
     def advance(self, n: int):
         """The last n stored rows become rows held (on the current stream)."""
@@ -432,24 +440,24 @@ class KVCache8:
         if q.dim() != 4:
             raise ValueError(f"q has shape {tuple(q.shape)}, expected [batch, n, heads, head_dim]")
         batch, n, heads, hd = q.shape
-        made = []
-        if out is None:
-            out = q.new_empty((batch, n, heads, hd))
-            made.append(out)
-            ld_o, o_between = heads * hd, n
-        else:
+        o_between = 0
+        if out is not None:
             ld_o, o_between = _rows_layout(out, "out", self.batch, heads, self.head_dim, torch.bfloat16, n)
             self._here("out", out)
-        if lse is None:
-            lse = self.k_scale.new_empty((batch, heads, n))
-            made.append(lse)
-        else:
+        if lse is not None:
             self._check("lse", lse, torch.float32, (batch, heads, n))
             self._here("lse", lse)
-        desc, need, ld = self._query(q, n_new, causal, max_len, softmax_scale, o_between)
+        desc, ld, need, like_o, like_lse, like_ws = self._query(q, n_new, causal, max_len, softmax_scale, o_between)
+        made = []
+        if out is None:
+            out, ld_o = torch.empty_like(like_o, memory_format=torch.contiguous_format), heads * hd
+            made.append(out)
+        if lse is None:
+            lse = torch.empty_like(like_lse, memory_format=torch.contiguous_format)
+            made.append(lse)
         if n == 0:
             return out, lse
-        ws, fresh = self._workspace(need, workspace)
+        ws, fresh = self._workspace(need, like_ws, workspace)
         self._call("cosmot_kv8_attention", desc, q.data_ptr(), ld, out.data_ptr(), ld_o, lse.data_ptr(), ptr(ws),
                    0 if ws is None else ws.numel(), self._stream(stream, *made, fresh))
         return out, lse
@@ -459,7 +467,7 @@ class KVCache8:
         """weight [batch, n_kv_heads, blocks] = decay * weight + the attention
         weight of q's rows for each block; lse as `attend` gave it for the same
         query.  Returns weight."""
-        desc, _, ld = self._query(q, n_new, causal, max_len, softmax_scale)
+        desc, ld, *_ = self._query(q, n_new, causal, max_len, softmax_scale)
         self._check("lse", lse, torch.float32, (self.batch, q.shape[2], q.shape[1]))
         self._check("weight", weight, torch.float32, (self.batch, self.n_kv_heads, self.n_blocks))
         self._here("lse", lse)
@@ -479,9 +487,9 @@ class KVCache8:
         self._check("weight", weight, torch.float32, (self.batch, self.n_kv_heads, self.n_blocks))
         self._here("weight", weight)
         w_out, lens = (weight, self.lens) if in_place else (torch.empty_like(weight), torch.empty_like(self.lens))
-        if self._evict_bytes is None:
-            self._evict_bytes = L.cosmot_kv8_evict_workspace(self.desc)
-        ws, fresh = self._workspace(self._evict_bytes, workspace)
+        if self._evict_like is None:
+            self._evict_like = self._shape((L.cosmot_kv8_evict_workspace(self.desc),), torch.uint8)
+        ws, fresh = self._workspace(self._evict_like.numel(), self._evict_like, workspace)
         made = (fresh,) if in_place else (fresh, w_out, lens)
         self._call("cosmot_kv8_evict", weight.data_ptr(), keep_blocks, first_rows, last_rows, w_out.data_ptr(),
                    lens.data_ptr(), ws.data_ptr(), ws.numel(), self._stream(stream, *made))
