@@ -368,6 +368,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t s_addr = tmem_base + ((uint32_t)lane_base << 16) + C::s_col(t);
     const uint32_t o_addr = tmem_base + ((uint32_t)lane_base << 16) + C::o_col(t);
     const int32_t lim = valid ? row_limit(p, r, len) : kend;  // padding rows see all: they never force the masks
+    const bool live = __any_sync(0xffffffffu, valid);  // the warp has a row to answer for
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     if (t == 0 || two) {
@@ -380,6 +381,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           break;
         }
         tc_fence_after();
+        if (!live) {  // what P and O hold in these lanes reaches no other row
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar_p_half + 8 * t);
+            mbar_arrive(bar_p_full + 8 * t);
+          }
+          continue;
+        }
         uint32_t s[128];
         tmem_ld32(s_addr + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
         tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
@@ -951,7 +961,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
           }
           if (ls == -INFINITY) lim = 0;  // a row that saw nothing is hidden from every key
           const bool masked = kbase + kTile > lim;
-          const bool any = __any_sync(0xffffffffu, lim > kbase);  // (no key of a tile behind the end)
+          // (not so for a tile of keys behind the end, nor for a warp whose rows are not there)
+          const bool any = __any_sync(0xffffffffu, lim > kbase && row < tile_rows && (int64_t)(w.i0 + i) * q_tile + qr < p.n_q);
           ok = warp_wait(bar_s_full + 8 * phase, ((n + i) >> 1) & 1, p.status, kWhereKv8Softmax);
           if (!ok) break;
           tc_fence_after();
