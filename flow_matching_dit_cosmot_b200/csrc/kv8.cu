@@ -287,11 +287,11 @@ __global__ void __launch_bounds__(kSelectThreads)
 
 // Blocks move towards the front: the source of the j-th kept block is list[j]
 // >= j, ascending.  A thread owns one 16-byte piece of one row of every block
-// and walks j upwards; it has begun to read the sources of block j and of the
-// kMoveRing - 2 after it before it writes block j, and no later source is a
-// block that it has written, so the move is in place without any thread waiting
+// and walks j upwards, kMoveTurn blocks a turn; it has begun to read the sources
+// of a turn and of the ones after it before it writes the turn's blocks, and no
+// later source is a block that it has written, so the move is in place without any thread waiting
 // for another.  The pieces wait in the thread's own slots of shared memory.
-constexpr int kMoveThreads = 64, kMoveRing = 24;
+constexpr int kMoveThreads = 128, kMoveTurn = 2, kMoveRing = 24;
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ Cache c,
                                                                   const EvictPlan* plan,
@@ -314,27 +314,44 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   const int32_t lo = pl.first, end = pl.count - (r >= part ? 1 : 0);
   __shared__ __align__(16) uint4 ring[kMoveRing][kMoveThreads];
   const uint32_t at = smem_u32(&ring[0][threadIdx.x]);
-  auto read = [&](int32_t j, int slot) {
-    if (j < end)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + slot * (kMoveThreads * 16)),
-                   "l"(base + load_global(src + j) * step)
-                   : "memory");
+  // the list is read one turn ahead: its latency would pace the thread
+  int32_t next[kMoveTurn];
+  auto look = [&](int32_t j) {
+#pragma unroll
+    for (int i = 0; i < kMoveTurn; ++i) next[i] = j + i < end ? src[j + i] : 0;
+  };
+  auto read = [&](int32_t j, int slot) {  // kMoveTurn blocks from j on, whose sources `next` holds
+#pragma unroll
+    for (int i = 0; i < kMoveTurn; ++i)
+      if (j + i < end)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + (slot * kMoveTurn + i) * (kMoveThreads * 16)),
+                     "l"(base + next[i] * step)
+                     : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  constexpr int kTurns = kMoveRing / kMoveTurn;  // on their way at any time
+  look(lo);
 #pragma unroll
-  for (int i = 0; i < kMoveRing - 1; ++i) read(lo + i, i);
+  for (int i = 0; i < kTurns - 1; ++i) {
+    read(lo + i * kMoveTurn, i);
+    look(lo + (i + 1) * kMoveTurn);
+  }
   int slot = 0;
-#pragma unroll 4
-  for (int32_t j = lo; j < end; ++j) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kMoveRing - 2) : "memory");
-    uint4 x;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                 : "r"(at + slot * (kMoveThreads * 16))
-                 : "memory");
-    *reinterpret_cast<uint4*>(base + j * step) = x;
-    read(j + kMoveRing - 1, slot == 0 ? kMoveRing - 1 : slot - 1);
-    slot = slot == kMoveRing - 1 ? 0 : slot + 1;
+#pragma unroll 2
+  for (int32_t j = lo; j < end; j += kMoveTurn) {
+    read(j + (kTurns - 1) * kMoveTurn, slot == 0 ? kTurns - 1 : slot - 1);
+    look(j + kTurns * kMoveTurn);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kTurns - 1) : "memory");
+#pragma unroll
+    for (int i = 0; i < kMoveTurn; ++i) {
+      uint4 x;
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                   : "r"(at + (slot * kMoveTurn + i) * (kMoveThreads * 16))
+                   : "memory");
+      if (j + i < end) *reinterpret_cast<uint4*>(base + (j + i) * step) = x;
+    }
+    slot = slot == kTurns - 1 ? 0 : slot + 1;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
@@ -553,7 +570,7 @@ extern "C" cosmot_status cosmot_kv8_evict(const cosmot_kv8_cache* cache, const f
                                 dim3(kv8::kSelectThreads), 0, s, nullptr, c, weight, keep_blocks, first_rows, last_rows,
                                 weight_out, plan, list, status));
   if (st != COSMOT_OK) return st;
-  const unsigned slices = (unsigned)(c.block * c.hd / 16 / kv8::kMoveThreads);  // 64 .. 1024 pieces
+  const unsigned slices = (unsigned)((c.block * c.hd / 16 + kv8::kMoveThreads - 1) / kv8::kMoveThreads);  // 64 .. 1024 pieces
   return launch_status(launch_pdl(kv8::evict_move_kernel, dim3(slices, (unsigned)(c.batch * c.n_kv), 2),
                                   dim3(kv8::kMoveThreads), 0, s, nullptr, c, (const kv8::EvictPlan*)plan,
                                   (const int32_t*)list, lens_out));
