@@ -681,10 +681,16 @@ cosmot_status rows_weigh(const Cache& c, const Query& p0, float decay, float* we
   if (chunk < span) chunk = span;
   p.chunk = (int32_t)chunk;
   const dim3 grid((unsigned)((c.capacity + chunk - 1) / chunk), (unsigned)heads);
-  return launch_status(c.hd == 128 ? launch_pdl(rows_weigh_kernel<128, 1>, grid, dim3(32 * kWarps), WeighRing<128>::kSmem, s,
-                                                nullptr, c, p, decay, weight)
-                                   : launch_pdl(rows_weigh_kernel<64, 1>, grid, dim3(32 * kWarps), WeighRing<64>::kSmem, s,
-                                                nullptr, c, p, decay, weight));
+  const bool one = rows_tiles(p) == 1;
+  if (c.hd == 128)
+    return launch_status(one ? launch_pdl(rows_weigh_kernel<128, 1>, grid, dim3(32 * kWarps), WeighRing<128>::kSmem, s,
+                                          nullptr, c, p, decay, weight)
+                             : launch_pdl(rows_weigh_kernel<128, 2>, grid, dim3(32 * kWarps), WeighRing<128>::kSmem, s,
+                                          nullptr, c, p, decay, weight));
+  return launch_status(one ? launch_pdl(rows_weigh_kernel<64, 1>, grid, dim3(32 * kWarps), WeighRing<64>::kSmem, s, nullptr,
+                                        c, p, decay, weight)
+                           : launch_pdl(rows_weigh_kernel<64, 2>, grid, dim3(32 * kWarps), WeighRing<64>::kSmem, s, nullptr,
+                                        c, p, decay, weight));
 }
 
 }  // namespace kv8

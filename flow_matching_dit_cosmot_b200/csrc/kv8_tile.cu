@@ -597,13 +597,14 @@ __global__ void __launch_bounds__(kTileJoinThreads) tile_join_kernel(const __gri
 }
 
 // ------------------------------------------------------------------ weighing
-// Warp 0 loads the queries' tiles (TMA), warp 1 issues the products, warps 2-3
-// widen the next item's keys, four warpgroups own the rows of two query tiles
-// x two key tiles; warp 3 adds their sums up, two items behind.  Items (256 keys
-// of a sequence and key head) go round the CTAs; nothing drains between two.
-// Registers: 128 x kWeighRegsIo + 512 x kWeighRegsRows out of the launch's pool.
-constexpr int kWeighThreads = 640;
-constexpr int kWeighRegsIo = 64, kWeighRegsRows = 104;
+// Warp 0 loads the queries' tiles (TMA), warp 1 issues the products, warps 2-7
+// widen the next item's keys, four warpgroups (warps 8-23) own the rows of two
+// query tiles x two key tiles; warp 3 adds their sums up, two items behind.
+// Items (256 keys of a sequence and key head) go round the CTAs; nothing drains
+// between two.
+// Registers: 256 x kWeighRegsIo + 512 x kWeighRegsRows out of the launch's pool.
+constexpr int kWeighThreads = 768, kWeighConvWarps = 6;
+constexpr int kWeighRegsIo = 64, kWeighRegsRows = 88;
 constexpr int kWeighMaxCluster = 4;
 constexpr int kQSlots = 3;
 constexpr int kPolyPairs = 2;  // of 8 pairs of exponentials, those on the FMA pipe
@@ -727,7 +728,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_s_full + 8 * s, 1);
       mbar_init(bar_s_empty + 8 * s, 8);
-      mbar_init(bar_k_full + 8 * s, 2);
+      mbar_init(bar_k_full + 8 * s, kWeighConvWarps);
       mbar_init(bar_k_empty + 8 * s, 1);
       mbar_init(bar_sum_full + 8 * s, 16);
       mbar_init(bar_sum_empty + 8 * s, 1);
@@ -739,9 +740,9 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  if (warp >= 4 && tile_rows < kTile) {  // the rows of a query tile that TMA never writes
+  if (warp >= 8 && tile_rows < kTile) {  // the rows of a query tile that TMA never writes
     const int pieces = (kTile - tile_rows) * (HD / 8);
-    for (int i = (int)threadIdx.x - 128; i < kQSlots * pieces; i += 512) {
+    for (int i = (int)threadIdx.x - 256; i < kQSlots * pieces; i += 512) {
       const int q = i % pieces;
       st_shared16(sQ + (i / pieces) * C::kTileBytes + sw_offset(tile_rows + q / (HD / 8), q % (HD / 8)), 0, 0, 0, 0);
     }
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
 
-  if (warp < 4) {
+  if (warp < 8) {
   setmaxnreg_dec<kWeighRegsIo>();
   if (warp == 0) {
     tma_prefetch_desc(&tmap_q);
@@ -819,8 +820,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     umma_commit_if(leader, bar_done);
     warp_wait(bar_done, 0, p.status, kWhereKv8Drain);
   } else {
-    // keys to bf16 (exact), rows behind the end zero; the two warps take four (hd 64: eight) rows in turn
-    constexpr int kRows = HD == 128 ? 4 : 8, kAhead = 4;
+    // keys to bf16 (exact), rows behind the end zero; the warps take four (hd 64: eight) rows in turn
+    constexpr int kRows = HD == 128 ? 4 : 8, kStep = kWeighConvWarps * kRows, kAhead = 4;
     const int u = HD == 128 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3;
     const int row0 = (warp - 2) * kRows + (HD == 128 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane >> 2);
     int done = 0, live = 0, added = 0;  // items converted, items with keys, items whose sums were added up
@@ -877,17 +878,18 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         const uint32_t dst = sK + (done & 1) * 2 * C::kTileBytes;
         ok = warp_wait(bar_k_empty + 8 * (done & 1), ((done >> 1) & 1) ^ 1, p.status, kWhereKv8Widen);
         const int rows = w.two ? 2 * kTile : kTile;
-        for (int r0 = row0; r0 < rows && ok; r0 += 2 * kRows * kAhead) {
+        for (int r0 = row0; r0 < rows && ok; r0 += kStep * kAhead) {
           uint4 x[kAhead];
 #pragma unroll
           for (int i = 0; i < kAhead; ++i) {
-            const int row = r0 + 2 * kRows * i;
+            const int row = r0 + kStep * i;
             x[i] = make_uint4(0, 0, 0, 0);
             if (w.k0 + row < w.k_end) x[i] = load_global(reinterpret_cast<const uint4*>(src + (int64_t)(w.k0 + row) * c.ld));
           }
 #pragma unroll
           for (int i = 0; i < kAhead; ++i) {
-            const int row = r0 + 2 * kRows * i;
+            const int row = r0 + kStep * i;
+            if (row >= rows) break;
             const uint32_t* z = reinterpret_cast<const uint32_t*>(&x[i]);
             uint32_t y[8];
 #pragma unroll
@@ -921,7 +923,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   }
   } else {
     setmaxnreg_inc<kWeighRegsRows>();
-    const int wg = (warp - 4) >> 2, t = wg & 1, phase = wg >> 1;
+    const int wg = (warp - 8) >> 2, t = wg & 1, phase = wg >> 1;
     const int lane_base = (warp & 3) * 32, row = lane_base + lane;
     const int32_t qr = row / p.group, hr = row % p.group;  // query and head of this row in a tile
     const uint32_t addr = tmem_base + ((uint32_t)lane_base << 16) + 128u * wg;
@@ -971,19 +973,17 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
             if (lane == 0) mbar_arrive(bar_s_empty + 8 * phase);
             continue;
           }
-          uint32_t s[2][32];
-          tmem_ld32(addr, s[0]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
+            // (four warps a sub-partition cover the loads; a second buffer of 32 measured no faster)
+            uint32_t x[32];
+            tmem_ld32(addr + 32 * q, x);
             tmem_ld_wait();
-            if (q < 3) {
-              tmem_ld32(addr + 32 * (q + 1), s[(q + 1) & 1]);
-            } else {  // S is in registers: the next product may overwrite it
+            if (q == 3) {  // S is in registers: the next product may overwrite it
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(bar_s_empty + 8 * phase);
             }
-            uint32_t(&x)[32] = s[q & 1];
             if (masked) {
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
@@ -1118,7 +1118,7 @@ cosmot_status launch_attention(const Cache& c, const Query& p, const TilePlan& t
 template <int HD>
 cosmot_status launch_weigh(const Cache& c, const Query& p, float decay, float* weight, int32_t max_len, cudaStream_t s) {
   static uint64_t done = 0;
-  cosmot_status st = prepare(tile_weigh_kernel<HD>, WeighCfg<HD>::kSmem, 128 * kWeighRegsIo + 512 * kWeighRegsRows,
+  cosmot_status st = prepare(tile_weigh_kernel<HD>, WeighCfg<HD>::kSmem, 256 * kWeighRegsIo + 512 * kWeighRegsRows,
                              kWeighThreads, done);
   if (st != COSMOT_OK) return st;
   const int32_t q_tile = kTile / p.group;
