@@ -607,6 +607,7 @@ constexpr int kWeighThreads = 768, kWeighConvWarps = 6;
 constexpr int kWeighRegsIo = 64, kWeighRegsRows = 88;
 constexpr int kWeighMaxCluster = 4;
 constexpr int kQSlots = 3;
+constexpr int kWeighLens = 64;
 constexpr int kPolyPairs = 2;  // of 8 pairs of exponentials, those on the FMA pipe
 
 template <int HD>
@@ -615,7 +616,8 @@ struct WeighCfg {
   static constexpr int kBars = (4 + kQSlots) * kTileBytes;  // two buffers of two key tiles, the queries' ring
   static constexpr int kSums = kBars + 192;                 // [2][4 warpgroups][4 warps][8 groups]
   static constexpr int kParts = kSums + 2 * 4 * 4 * 8 * 4;  // [2][cluster][16 groups]
-  static constexpr int kSmem = kParts + 2 * kWeighMaxCluster * 16 * 4 + 1024;
+  static constexpr int kLens = kParts + 2 * kWeighMaxCluster * 16 * 4;  // the first sequences' lengths
+  static constexpr int kSmem = kLens + kWeighLens * 4 + 1024;
   static constexpr int kBoxK = 2 * kBoxBytes;  // 256 keys x 64 columns
   static constexpr uint32_t kIdesc2 = idesc_bf16_f32(kTile, 2 * kTile, false, false);  // both key tiles at once
   static constexpr uint32_t kIdesc1 = idesc_bf16_f32(kTile, kTile, false, false);
@@ -667,36 +669,42 @@ struct WeighItem {
   bool two;
 };
 
-__device__ __forceinline__ WeighItem weigh_item(const Cache& c, const Query& p, int64_t item, int32_t q_tile, int32_t rank,
-                                                int32_t ranks) {
+// (32-bit arithmetic: every warp does this for every item)
+__device__ __forceinline__ WeighItem weigh_item(const Cache& c, const Query& p, uint32_t item, int32_t q_tile, int32_t n_all,
+                                                int32_t rank, int32_t ranks, const int32_t* lens) {
   WeighItem w;
-  const int32_t heads = c.batch * c.n_kv;  // one key range of every head, then the next
+  const uint32_t heads = (uint32_t)c.batch * (uint32_t)c.n_kv;  // one key range of every head, then the next
   w.bg = (int32_t)(item % heads);
-  w.b = w.bg / c.n_kv;
+  w.b = c.batch == 1 ? 0 : (int32_t)((uint32_t)w.bg / (uint32_t)c.n_kv);
   w.k0 = (int32_t)(item / heads) * 2 * kTile;
-  w.len = __shfl_sync(0xffffffffu, shown_rows(c, w.b, p.n_new, p.status, threadIdx.x == 0 && rank == 0), 0);
+  w.len = w.b < kWeighLens ? lens[w.b] : shown_rows(c, w.b, p.n_new, p.status, threadIdx.x == 0 && rank == 0);
+  w.len = __shfl_sync(0xffffffffu, w.len, 0);
   w.k_end = min(w.len, w.k0 + 2 * kTile);
   if (w.k0 >= w.len) w.k_end = w.k0;
   w.two = w.k0 + kTile < w.k_end;
   // query tiles that see a key of the range (causal: the last ones), shared by the cluster
-  const int32_t n_all = (int32_t)((p.n_q + q_tile - 1) / q_tile);
   int32_t first = w.k_end > w.k0 ? 0 : n_all;
   if (p.causal && w.k_end > w.k0) {  // query i sees keys <= len - n_q + i
-    const int64_t q_first = (int64_t)w.k0 - (w.len - p.n_q);
-    if (q_first > 0) first = (int32_t)(q_first / q_tile);  // < n_all as k0 < len
+    const int32_t q_first = w.k0 - (w.len - (int32_t)p.n_q);
+    if (q_first > 0) first = (int32_t)((uint32_t)q_first / (uint32_t)q_tile);  // < n_all as k0 < len
   }
-  w.i0 = first + (int32_t)((int64_t)(n_all - first) * rank / ranks);
-  w.n_i = first + (int32_t)((int64_t)(n_all - first) * (rank + 1) / ranks) - w.i0;
+  w.i0 = first;
+  w.n_i = n_all - first;
+  if (ranks > 1) {
+    const int32_t n = n_all - first;
+    w.i0 = first + (int32_t)((int64_t)n * rank / ranks);
+    w.n_i = first + (int32_t)((int64_t)n * (rank + 1) / ranks) - w.i0;
+  }
   return w;
 }
 
 // q_tile: queries of a tile (kTile / group), its rows q_tile * group <= 128;
-// ranges: key ranges of 256 in the capacity.
+// n_all: the query tiles; ranges: key ranges of 256 in the capacity.
 template <int HD>
 __global__ void __launch_bounds__(kWeighThreads, 1)
     tile_weigh_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ Cache c,
                       const __grid_constant__ Query p, float decay, float* weight, int32_t q_tile,
-                      int32_t ranges) {
+                      int32_t n_all, int32_t ranges) {
   using C = WeighCfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -715,10 +723,11 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kQSlots + 13);
   float* sums = reinterpret_cast<float*>(smem + C::kSums);
   float* parts = reinterpret_cast<float*>(smem + C::kParts);
+  int32_t* lens = reinterpret_cast<int32_t*>(smem + C::kLens);
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int32_t ranks = gridDim.y, rank = blockIdx.y;  // the cluster runs along y
-  const int64_t items = (int64_t)c.batch * c.n_kv * ranges;
+  const uint32_t items = (uint32_t)c.batch * (uint32_t)c.n_kv * (uint32_t)ranges;  // < 2^31
   const int32_t tile_rows = q_tile * p.group;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kQSlots; ++s) {
@@ -750,6 +759,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   }
   pdl_trigger();
   pdl_wait();
+  for (int i = (int)threadIdx.x; i < kWeighLens && i < c.batch; i += kWeighThreads)
+    lens[i] = shown_rows(c, i, p.n_new, p.status, blockIdx.x == 0 && rank == 0);
   tc_fence_before();
   if (ranks > 1)
     cluster_sync();  // every CTA of the cluster has started before anything is written to it
@@ -764,8 +775,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     tma_prefetch_desc(&tmap_q);
     int n = 0;  // tiles so far
     bool ok = true;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-      const WeighItem w = weigh_item(c, p, item, q_tile, rank, ranks);
+    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+      const WeighItem w = weigh_item(c, p, item, q_tile, n_all, rank, ranks, lens);
       for (int i = 0; i < w.n_i && ok; ++i, ++n) {
         const int slot = n % kQSlots;
         ok = warp_wait(bar_q_empty + 8 * slot, ((n / kQSlots) & 1) ^ 1, p.status, kWhereKv8Widen);
@@ -791,8 +802,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     const uint32_t leader = elect_one();
     int n = 0, done = 0;  // query tiles, items
     bool ok = true;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-      const WeighItem w = weigh_item(c, p, item, q_tile, rank, ranks);
+    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+      const WeighItem w = weigh_item(c, p, item, q_tile, n_all, rank, ranks, lens);
       if (w.n_i > 0 && ok) {
         const int kbuf = done & 1;
         const uint32_t idesc = w.two ? C::kIdesc2 : C::kIdesc1;
@@ -821,7 +832,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     warp_wait(bar_done, 0, p.status, kWhereKv8Drain);
   } else {
     // keys to bf16 (exact), rows behind the end zero; the warps take four (hd 64: eight) rows in turn
-    constexpr int kRows = HD == 128 ? 4 : 8, kStep = kWeighConvWarps * kRows, kAhead = 4;
+    constexpr int kRows = HD == 128 ? 4 : 8, kStep = kWeighConvWarps * kRows, kAhead = 6;
     const int u = HD == 128 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3;
     const int row0 = (warp - 2) * kRows + (HD == 128 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane >> 2);
     int done = 0, live = 0, added = 0;  // items converted, items with keys, items whose sums were added up
@@ -867,25 +878,28 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       }
       __syncwarp();
     };
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-      const WeighItem w = weigh_item(c, p, item, q_tile, rank, ranks);
+    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+      const WeighItem w = weigh_item(c, p, item, q_tile, n_all, rank, ranks, lens);
+      const uint8_t* src = c.k + (int64_t)w.b * c.bstride * c.ld + (int64_t)(w.bg % c.n_kv) * HD + u * 16;
+      const int rows = w.two ? 2 * kTile : kTile;
+      uint4 x[kAhead];
+      auto load = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int row = r0 + kStep * i;
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (w.k0 + row < w.k_end) x[i] = load_global(reinterpret_cast<const uint4*>(src + (int64_t)(w.k0 + row) * c.ld));
+        }
+      };
+      if (w.n_i > 0) load(row0);  // on their way while the buffer empties
       if (ranks == 1 && live - added == 2) {  // its keys' buffer is free about when its sums are there
         add_up(last[0], added++);
         last[0] = last[1];
       }
       if (w.n_i > 0 && ok) {
-        const uint8_t* src = c.k + (int64_t)w.b * c.bstride * c.ld + (int64_t)(w.bg % c.n_kv) * HD + u * 16;
         const uint32_t dst = sK + (done & 1) * 2 * C::kTileBytes;
         ok = warp_wait(bar_k_empty + 8 * (done & 1), ((done >> 1) & 1) ^ 1, p.status, kWhereKv8Widen);
-        const int rows = w.two ? 2 * kTile : kTile;
         for (int r0 = row0; r0 < rows && ok; r0 += kStep * kAhead) {
-          uint4 x[kAhead];
-#pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            const int row = r0 + kStep * i;
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (w.k0 + row < w.k_end) x[i] = load_global(reinterpret_cast<const uint4*>(src + (int64_t)(w.k0 + row) * c.ld));
-          }
 #pragma unroll
           for (int i = 0; i < kAhead; ++i) {
             const int row = r0 + kStep * i;
@@ -903,6 +917,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
             st_shared16(dst + sw_offset<C::kBoxK>(row, 2 * u), y[0], y[1], y[2], y[3]);
             st_shared16(dst + sw_offset<C::kBoxK>(row, 2 * u + 1), y[4], y[5], y[6], y[7]);
           }
+          if (r0 + kStep * kAhead < rows) load(r0 + kStep * kAhead);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -925,23 +940,25 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     setmaxnreg_inc<kWeighRegsRows>();
     const int wg = (warp - 8) >> 2, t = wg & 1, phase = wg >> 1;
     const int lane_base = (warp & 3) * 32, row = lane_base + lane;
+    const int block_shift = 31 - __clz(c.block);
     const int32_t qr = row / p.group, hr = row % p.group;  // query and head of this row in a tile
     const uint32_t addr = tmem_base + ((uint32_t)lane_base << 16) + 128u * wg;
     int n = 0, done = 0;  // query tiles, items
     bool ok = true;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-      const WeighItem w = weigh_item(c, p, item, q_tile, rank, ranks);
+    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+      const WeighItem w = weigh_item(c, p, item, q_tile, n_all, rank, ranks, lens);
       if (w.k_end == w.k0) {
         if (ranks > 1) cluster_sync();
         continue;
       }
       const int32_t kbase = w.k0 + t * kTile;
       float acc[8], f[8];
+      const float* ks = c.k_scale + (int64_t)w.bg * c.n_blocks;
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
         acc[g] = 0.f;
         const int32_t key = kbase + 16 * g;
-        f[g] = key < w.k_end ? p.scale_log2 * load_global(c.k_scale + (int64_t)w.bg * c.n_blocks + key / c.block) : 0.f;
+        f[g] = key < w.k_end ? p.scale_log2 * load_global(ks + (key >> block_shift)) : 0.f;
       }
       const float* lse_row = p.lse + ((int64_t)w.b * p.n_heads + (w.bg % c.n_kv) * p.group + hr) * p.n_q;
       {
@@ -1129,6 +1146,7 @@ cosmot_status launch_weigh(const Cache& c, const Query& p, float decay, float* w
   const int64_t heads = (int64_t)c.batch * c.n_kv, n_all = (p.n_q + q_tile - 1) / q_tile;
   const int32_t ranges = (c.capacity + 2 * kTile - 1) / (2 * kTile);
   const int64_t live = heads * (((int64_t)max_len + 2 * kTile - 1) / (2 * kTile)), items = heads * ranges, sms = num_sms();
+  if (items > INT32_MAX / 2) return COSMOT_ERR_UNSUPPORTED;
   // a key range's queries are shared by a cluster where there are fewer key ranges than SMs
   int ranks = 1;
   while (ranks < kWeighMaxCluster && live * ranks * 2 <= sms && n_all >= 4 * ranks) ranks *= 2;
@@ -1139,7 +1157,7 @@ cosmot_status launch_weigh(const Cache& c, const Query& p, float decay, float* w
   cl.val.clusterDim.z = 1;
   const dim3 grid((unsigned)(items < sms / ranks ? items : sms / ranks), (unsigned)ranks);
   return launch_status(launch_pdl(tile_weigh_kernel<HD>, grid, dim3(kWeighThreads), WeighCfg<HD>::kSmem, s, &cl, map, c, p,
-                                  decay, weight, q_tile, ranges));
+                                  decay, weight, q_tile, (int32_t)n_all, ranges));
 }
 
 }  // namespace
