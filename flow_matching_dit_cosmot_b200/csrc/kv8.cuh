@@ -70,12 +70,17 @@ __device__ __forceinline__ int32_t shown_rows(const Cache& c, int32_t b, int32_t
   return held < 0 ? 0 : c.capacity;
 }
 
+// Query and head (within its key head's group) of packed row r.  n_rows < 2^30:
+// 32-bit division, which a warp's short prologue notices.
+__device__ __forceinline__ int32_t row_query(const Query& p, int64_t r) { return (int32_t)((uint32_t)r / (uint32_t)p.group); }
+__device__ __forceinline__ int32_t row_head(const Query& p, int64_t r) { return (int32_t)((uint32_t)r % (uint32_t)p.group); }
+
 // First hidden key of packed row r (n_rows and beyond: padding, sees nothing).
 __device__ __forceinline__ int32_t row_limit(const Query& p, int64_t r, int32_t len) {
   if (r >= p.n_rows) return 0;
   if (!p.causal) return len;
-  const int64_t lim = (int64_t)len - p.n_q + r / p.group + 1;
-  return lim < 0 ? 0 : (int32_t)(lim < len ? lim : len);
+  const int32_t lim = len - (int32_t)p.n_q + row_query(p, r) + 1;
+  return lim < 0 ? 0 : (lim < len ? lim : len);
 }
 
 // (e4m3, e4m3) -> (f16, f16), exact; byte 0 goes to the low half.

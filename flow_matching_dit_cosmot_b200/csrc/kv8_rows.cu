@@ -126,8 +126,8 @@ __device__ __forceinline__ void load_q_tile(const Cache& c, const Query& p, int3
   for (int n = 0; n < NT; ++n) {
     const int64_t r = r0 + 8 * n + g;
     const bool valid = r < p.n_rows;
-    const int64_t qi = valid ? r / p.group : 0;
-    const int32_t h = kvh * p.group + (int32_t)(valid ? r % p.group : 0);
+    const int64_t qi = valid ? row_query(p, r) : 0;
+    const int32_t h = kvh * p.group + (valid ? row_head(p, r) : 0);
     const float f = p.scale_log2 * load_q_row<HD>(p.q + (b * p.q_bstride + qi) * p.ld_q + (int64_t)h * HD, valid, j, q[n]);
     fac[n][0] = __shfl_sync(0xffffffffu, f, 8 * j);
     fac[n][1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
@@ -407,8 +407,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
       if (col == 0) p.part_ml[pr] = make_float2(lsum == 0.f ? -INFINITY : ref, lsum);
     } else {
       const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-      const int64_t qi = r / p.group;
-      const int32_t h = kvh * p.group + (int32_t)(r % p.group);
+      const int64_t qi = row_query(p, r);
+      const int32_t h = kvh * p.group + row_head(p, r);
       if (!dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store)) continue;
       *reinterpret_cast<uint2*>(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col) =
           make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
@@ -487,8 +487,8 @@ __global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const __grid_co
     acc.w += x.w;
   }
   const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-  const int64_t qi = r / p.group;
-  const int32_t h = kvh * p.group + (int32_t)(r % p.group);
+  const int64_t qi = row_query(p, r);
+  const int32_t h = kvh * p.group + row_head(p, r);
   if (!dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store)) return;
   *reinterpret_cast<uint2*>(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col * 4) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -562,8 +562,8 @@ __global__ void __launch_bounds__(32 * kWarps) rows_weigh_kernel(const __grid_co
         lim[m][i] = len;
         lse[m][i] = INFINITY;  // rows that are not there: 2^-inf
         if (r < p.n_rows) {
-          const int64_t qi = r / p.group;
-          const int32_t h = kvh * p.group + (int32_t)(r % p.group);
+          const int64_t qi = row_query(p, r);
+          const int32_t h = kvh * p.group + row_head(p, r);
           lse[m][i] = p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] * kLog2e;
           lim[m][i] = lse[m][i] == -INFINITY ? 0 : row_limit(p, r, len);  // a row that saw nothing weighs nothing
         }

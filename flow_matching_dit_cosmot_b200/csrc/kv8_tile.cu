@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int lane_base = (warp & 3) * 32;   // TMEM lanes this warp may access
     const int64_t r = r0 + t * kTile + lane_base + lane;
     const bool valid = r < p.n_rows;
-    const int32_t qi = valid ? (int32_t)((uint32_t)r / (uint32_t)p.group) : 0;
+    const int32_t qi = valid ? row_query(p, r) : 0;
     const int32_t h = kvh * p.group + (valid ? (int32_t)r - qi * p.group : 0);
     // Q: a warp's 32 rows come into their places as bf16, whole rows at a time;
     // then every lane turns its own row into f16 where it lies.  Short loops: a
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kTileJoinThreads) tile_join_kernel(const __gri
     acc[3] = fmaf(f, x.w, acc[3]);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int32_t qi = (int32_t)((uint32_t)r / (uint32_t)p.group), h = kvh * p.group + (int32_t)r - qi * p.group;
+  const int32_t qi = row_query(p, r), h = kvh * p.group + (int32_t)r - qi * p.group;
   if (!dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store)) return;
   *reinterpret_cast<uint2*>(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col) =
       make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
