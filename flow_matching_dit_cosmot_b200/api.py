@@ -327,6 +327,7 @@ class KVCache8:
                                capacity, n_kv, hd, block, 0)
         self._ref = ctypes.byref(self.desc)
         self._plans = {}
+        self._one = {t: torch.empty((1,), dtype=t, device=self.device) for t in (torch.bfloat16, torch.float32, torch.uint8)}
         self._evict_like = None
 
     @classmethod
@@ -379,7 +380,7 @@ class KVCache8:
 
     def _shape(self, shape, dtype):
         """One element seen as a tensor of `shape`: torch.empty_like gives a new contiguous one."""
-        return torch.empty((1,), dtype=dtype, device=self.device).expand(shape)
+        return self._one[dtype].expand(shape)
 
     def _workspace(self, need: int, like: Optional[torch.Tensor], workspace: Optional[torch.Tensor]):
         """(tensor, made here): the caller's workspace, or one for this call."""

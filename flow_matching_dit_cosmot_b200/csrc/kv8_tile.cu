@@ -3,19 +3,19 @@
 //
 // Attention.  One CTA per (sequence, key head, 256 packed query rows) and, for
 // the items of the last wave, per key split.  512 threads in four warpgroups:
-//   warp 0       owns TMEM and issues the MMAs from one thread:
+//   warp 0       owns TMEM and issues the MMAs:
 //                  S_t = Q_t K_j^T   (M 128, N 128, K head_dim; both in smem)
 //                  O_t += P_t V_j    (A = P in TMEM over S)
 //                in the order S0 S1 | PV0 S0' PV1 S1' | ..., so that one tile's
 //                products run beside the other tile's softmax.
-//   warps 4-7    read the cache's bytes (16 a load), widen them to f16 (exact)
-//                and write the 128-byte-swizzled tiles that the MMAs read, one
-//                K or V tile ahead in registers and four slots ahead in smem.
+//   warps 1-7    read the cache's bytes (16 a load), widen them to f16 (exact)
+//                and write the 128-byte-swizzled tiles that the MMAs read, a K
+//                and a V tile ahead in registers and four slots ahead in smem.
 //   warps 8-11   softmax of rows 0-127, warps 12-15 of rows 128-255, a row per
 //                thread; first they bring their rows of Q into smem as f16, by a
 //                power of two per row (its largest magnitude in [2^13, 2^14):
 //                exact down to 2^-31 of it).
-// The scales of a 128-key tile come as eight groups of 16 keys (block >= 16):
+// The scales of a 128-key tile come with its keys, one for each 128 / NG keys:
 //     x = s (q factor)(ks) + log2 vs,   p vs = 2^(x - m + 8)  (f16 in TMEM),
 // m the running maximum of x; it is followed only when it grows by more than
 // 2^7, so p vs stays below 2^15 and f16 keeps full precision down to 2^-22 of

@@ -1,13 +1,15 @@
 """The 8-bit cache's operators from their definitions, in 64 bits and row by
 row, sharing nothing with the kernels; and the error bounds of their outputs.
 
-Bounds.  The kernels form scores from exact operands (e4m3 bytes; bf16 queries
-split exactly down to 2^-18 of their row's largest magnitude, at half a step of
-2^-19) with float32 accumulation.  Adding n products in any order, each addition
-off by at most one unit of 2^-23 of the partial sum, is off by at most
-n 2^-23 sum|q k|; so a score is off by
+Bounds.  The kernels form scores from e4m3 bytes, which are exact in f16 and
+bf16, and from queries in bf16 or in f16 with their row's largest magnitude
+brought into [2^13, 2^14) by a power of two: bf16's 8 bits are exact there but
+for f16's subnormals, half a step of 2^-25, so 2^-38 of the largest.  Sums are
+float32.  Adding n products in any order, each addition off by at most one unit
+of 2^-23 of the partial sum, is off by at most n 2^-23 sum|q k|; so a score is
+off by
 
-    ds <= scale (hd 2^-23 sum|q k| + 2^-18 max|q| sum|k|) + 2^-22 |s|
+    ds <= scale (hd 2^-23 sum|q k| + 2^-38 max|q| sum|k|) + 2^-22 |s|
 
 (the last term: the factors applied to it in float32).  A softmax weight is
 then off by a factor exp(ds) and its rounding to f16 (2^-11; weights below
@@ -89,7 +91,7 @@ def attend(q, K, V, lens, causal, scale=None):
             k, v = K[b, :L, h // (H // g)], V[b, :L, h // (H // g)]
             s = q[b, :, h] @ k.T * scale
             ds = scale * (hd * 2.0 ** -23 * (q[b, :, h].abs() @ k.abs().T)
-                          + 2.0 ** -18 * q[b, :, h].abs().amax(-1, keepdim=True) * k.abs().sum(-1)) + 2.0 ** -22 * s.abs()
+                          + 2.0 ** -38 * q[b, :, h].abs().amax(-1, keepdim=True) * k.abs().sum(-1)) + 2.0 ** -22 * s.abs()
             s = s.masked_fill(~see, -math.inf)
             ds = (ds * see).amax(1)
             any_ = see.any(1)
@@ -129,7 +131,7 @@ def weigh(q, K, lse, lens, block, causal, weight, decay, scale=None):
             k = K[b, :L, kv]
             s = q[b, :, h] @ k.T * scale
             ds = scale * (hd * 2.0 ** -23 * (q[b, :, h].abs() @ k.abs().T)
-                          + 2.0 ** -18 * q[b, :, h].abs().amax(-1, keepdim=True) * k.abs().sum(-1))
+                          + 2.0 ** -38 * q[b, :, h].abs().amax(-1, keepdim=True) * k.abs().sum(-1))
             ls = lse[b, h][:, None]
             live = see & torch.isfinite(ls)
             p = torch.where(live, torch.exp(s - torch.where(torch.isfinite(ls), ls, 0.0)), 0.0)

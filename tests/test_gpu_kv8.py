@@ -494,3 +494,101 @@ def test_results_do_not_depend_on_the_batch_or_the_run():
     a, _ = c.attend(q)
     b, _ = c.attend(q)
     assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ corners
+
+def scattered(batch, cap, g, hd, block, lens, seed):
+    """A cache of random bytes and scales (powers of two)."""
+    c = A.KVCache8.empty(batch, cap, g, hd, block)
+    gen = torch.Generator("cuda").manual_seed(seed)
+    for t in (c.k, c.v):
+        u = t.view(torch.uint8)
+        u.copy_(torch.randint(0, 0x70, t.shape, generator=gen, device="cuda", dtype=torch.uint8))
+        u.bitwise_or_(torch.randint(0, 2, t.shape, generator=gen, device="cuda", dtype=torch.uint8) << 7)
+    for t in (c.k_scale, c.v_scale):
+        t.copy_(2.0 ** torch.randint(-9, -6, t.shape, generator=gen, device="cuda").float())
+    c.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    return c
+
+
+@pytest.mark.parametrize("lens,n,g,group,hd,block,causal", [
+    ([9000], 1, 200, 1, 64, 16, False),              # more blocks in a key range than scales kept beside it
+    ([50 + i for i in range(70)], 40, 1, 1, 64, 16, True),  # more sequences than lengths kept beside the items
+    ([200, 90], 2, 1, 136, 64, 32, False),           # more heads on a key head than a query tile has rows
+    ([200, 0, 90], 1, 2, 40, 128, 16, True),
+    ([40_000], 3, 1, 1, 128, 64, False),
+    ([2600], 34, 1, 4, 128, 128, True),              # one pair of query tiles, its keys split many ways
+    ([1], 300, 1, 2, 64, 16, True),                  # one key: all rows but the last see nothing
+])
+def test_corner_sizes(lens, n, g, group, hd, block, causal):
+    c = scattered(len(lens), max(lens) + 9, g, hd, block, lens, seed=110)
+    q = queries(111, len(lens), n, g * group, hd) * 0.2
+    _, lse = check_attend(c, q, lens, causal)
+    check_weigh(c, q, lse, lens, causal)
+
+
+@pytest.mark.parametrize("n", [1, 60])
+def test_an_output_of_odd_sixteen_byte_rows(n):
+    """Rows of o that start 16, not 32, bytes from a 32-byte boundary."""
+    c = scattered(1, 300, 2, 64, 16, [300], seed=112)
+    q = queries(113, 1, n, 4, 64)
+    want, _ = c.attend(q)
+    raw = torch.zeros((n * (4 * 64 + 8) + 8,), dtype=torch.bfloat16, device="cuda")
+    out = raw[8:].as_strided((1, n, 4, 64), (n * 264, 264, 64, 1))
+    c.attend(q, out=out)
+    assert torch.equal(out, want)
+
+
+def test_no_queries_still_decay_the_weights():
+    c = scattered(2, 100, 2, 64, 16, [100, 33], seed=114)
+    w = torch.ones((2, 2, c.n_blocks), device="cuda")
+    q = torch.zeros((16,), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((4,), device="cuda")
+    desc = L.Kv8Query(0, 0, 0, 2, 0, 0, 0, 0.0, 0)
+    L.cosmot_kv8_weigh(c.desc, desc, q.data_ptr(), 128, lse.data_ptr(), 0.25, w.data_ptr(),
+                       torch.cuda.current_stream().cuda_stream)
+    live = torch.arange(c.n_blocks, device="cuda") * 16 < c.lens[:, None]
+    assert torch.equal(w, torch.where(live[:, None], 0.25, 1.0).expand_as(w))
+    assert_device_ok()
+
+
+@pytest.mark.parametrize("n", [1, 150])
+def test_outputs_made_here_wait_for_the_current_stream(n):
+    """A call on another stream takes its outputs from the current stream's memory,
+    which may still be in use there."""
+    c = scattered(1, 2000, 2, 64, 64, [2000], seed=115)
+    q = queries(116, 1, n, 4, 64)
+    want, wl = c.attend(q)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    big = torch.ones((1 << 26,), device="cuda")
+    for _ in range(5):
+        busy = torch.empty_like(want)
+        for _ in range(20):
+            big.mul_(1.0)
+        busy.fill_(3.0)  # behind the work above, in memory that is free (to this stream) after the next line
+        del busy
+        o, lse = c.attend(q, stream=other)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("n", [1, 40, 150])
+def test_the_debug_build_gives_the_same_and_finds_nothing(n):
+    """Every store index is checked there."""
+    D, R = L.lib_debug(), L.lib()
+    outs = []
+    for lib in (R, D):
+        L._lib = lib
+        try:
+            c = filled(2, 700, 2, 64, 16, [333, 77], seed=117)
+            w = c.empty_weight()
+            o, lse = _step(c, {"qkv": rows(118, 2, n, 8, 64)}, w, n, 9)
+            torch.cuda.synchronize()
+            assert_device_ok()
+        finally:
+            L._lib = R
+        outs.append((o, lse, w, c.lens, c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_scale.nan_to_num()))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
