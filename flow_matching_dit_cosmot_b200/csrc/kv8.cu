@@ -16,7 +16,8 @@ namespace kv8 {
 // bound: HBM (4 bytes read and 2 written for each K and V element).  18,978 rows
 // x 32 heads of 128: 88 us = 5.3 TB/s.  256 threads at four CTAs an SM took 82
 // us where 512 took 99 and 128 the same; magnitudes on packed bits saved 12 us
-// (the float form kept the issue slots 72 % busy).
+// (the float form kept the issue slots 72 % busy).  1,560 rows: 10.8 us at six
+// CTAs an SM, 11.9 at four.
 constexpr int kStoreThreads = 256;
 
 // Largest of the CTA's values: magnitudes of bf16 order like their bits.
@@ -30,7 +31,7 @@ __device__ __forceinline__ uint32_t cta_max_bf16(uint32_t mag, uint32_t* part) {
 }
 
 template <int kUnits>
-__global__ void __launch_bounds__(kStoreThreads, 4)
+__global__ void __launch_bounds__(kStoreThreads, kUnits <= 4 ? 6 : 4)
     store_kernel(const __grid_constant__ Cache c, const __nv_bfloat16* ksrc,
                  const __nv_bfloat16* vsrc, int64_t ld_src, int64_t src_bstride, int32_t n, int* status) {
   pdl_trigger();
