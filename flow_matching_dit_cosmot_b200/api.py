@@ -300,6 +300,9 @@ class KVCache8:
 
     Every call runs on `stream` (default: the current one of the cache's device)
     and follows `lens` on the device, so it may be captured into a CUDA graph.
+    Outputs and workspaces that a call makes are its own; on another stream it
+    first waits for the current one, whose memory they are.  A workspace given by
+    the caller serves one call at a time.
     The library reports lengths outside the cache through the device status.
     """
 

@@ -653,12 +653,16 @@ void rows_plan(const Cache& c, Query& p, int32_t max_len) {
   p.splits = 1;
   p.chunk = max_len;
   if (tiles <= 0) return;
-  // as many key ranges as fill the SMs once (a batch of unequal lengths: four
-  // times, so that the long ones are not left alone), of 256 keys at least
-  const int64_t want = (int64_t)num_sms() * ctas_per_sm(rows_tiles(p)) * (c.batch > 1 ? 4 : 1) / tiles;
-  int64_t n = want < 1 ? 1 : (want > kMaxSplits ? kMaxSplits : want);
+  // As many key ranges as fill the SMs once (a batch of unequal lengths: four
+  // times, so that the long ones are not left alone).  A range has 256 keys at
+  // least: 768 keys x 8 key heads take 6.8 us so, 7.7 as one range, but 512 take
+  // 6.2 as one and 6.6 as two; and 1,024 where the rows alone fill half the SMs:
+  // 768 keys x 512 heads take 17 us as one range, 23 in ranges of 256.
+  const int64_t slots = (int64_t)num_sms() * ctas_per_sm(rows_tiles(p)), want = slots * (c.batch > 1 ? 4 : 1) / tiles;
+  const int64_t n = want < 1 ? 1 : (want > kMaxSplits ? kMaxSplits : want);
+  const int64_t least = 2 * tiles >= slots ? 1024 : (max_len <= 512 ? 512 : 256);
   int64_t chunk = ((max_len + n - 1) / n + 63) & ~int64_t(63);
-  if (chunk < 256) chunk = 256;
+  if (chunk < least) chunk = least;
   p.chunk = (int32_t)(chunk < INT32_MAX ? chunk : INT32_MAX);
   p.splits = (int32_t)((max_len + chunk - 1) / chunk);
   if (p.splits < 1) p.splits = 1;
