@@ -592,3 +592,33 @@ def test_the_debug_build_gives_the_same_and_finds_nothing(n):
         outs.append((o, lse, w, c.lens, c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_scale.nan_to_num()))
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+def test_the_python_layer_refuses_what_does_not_fit():
+    c = scattered(2, 100, 2, 64, 16, [100, 33], seed=120)
+    q = queries(121, 2, 3, 4, 64)
+    o, lse = c.attend(q)
+    w = c.empty_weight()
+    for call in (lambda: c.attend(q.float()), lambda: c.attend(q.cpu()), lambda: c.attend(q[:1]), lambda: c.attend(q[0]),
+                 lambda: c.attend(q, out=o[:, :2]), lambda: c.attend(q, out=o.float()), lambda: c.attend(q, lse=lse[:, :, :2]),
+                 lambda: c.attend(q, lse=lse.transpose(1, 2)), lambda: c.weigh(q, lse[:1], w), lambda: c.weigh(q, lse, w[:, :1]),
+                 lambda: c.weigh(q, lse, w.double()), lambda: c.weigh(q[:, :0], lse[:, :, :0], w), lambda: c.weigh(q, lse.cpu(), w),
+                 lambda: c.evict(w[:, :, 1:], 2), lambda: c.evict(w.cpu(), 2), lambda: c.store(q, q),
+                 lambda: c.store(q[:, :, :2], q[:, :2, :2]), lambda: c.store(q[:, :, :2].float(), q[:, :, :2].float()),
+                 lambda: c.evict(w, 2, workspace=torch.empty((8,), dtype=torch.uint8, device="cuda")),
+                 lambda: A.KVCache8(c.k, c.v[:, :50], c.k_scale, c.v_scale, c.lens, 16),
+                 lambda: A.KVCache8(c.k, c.v, c.k_scale, c.v_scale, c.lens, 24),
+                 lambda: A.KVCache8(c.k, c.v, c.k_scale[:, :, 1:], c.v_scale, c.lens, 16),
+                 lambda: A.KVCache8(c.k, c.v, c.k_scale, c.v_scale, c.lens.long(), 16)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: c.attend(queries(121, 2, 3, 3, 64)), lambda: c.attend(q, n_new=101), lambda: c.attend(q, n_new=-1),
+                 lambda: c.attend(q, max_len=-1), lambda: c.attend(q, softmax_scale=-1.0), lambda: c.weigh(q, lse, w, decay=-1.0),
+                 lambda: c.evict(w, 0), lambda: c.evict(w, 2, first_rows=-1), lambda: c.store(*[rows(1, 2, 101, 2, 64)] * 2)):
+        with pytest.raises(L.CosmotError):
+            call()
+    empty, none = c.attend(q[:, :0])
+    assert empty.shape == (2, 0, 4, 64) and none.shape == (2, 4, 0)
+    c.store(q[:, :0, :2], q[:, :0, :2])
+    assert torch.equal(c.attend(q)[0], o)
+    assert_device_ok()

@@ -104,6 +104,24 @@ def test_bad_pointers_strides_and_workspaces_are_refused():
     assert lib.cosmot_kv8_attention(c, ctypes.byref(query(n_q=0)), 256, 512, 256, 512, None, None, 0, None) == L.COSMOT_OK
 
 
+@pytest.mark.parametrize("n_q,heads,capacity", [(1, 4, 100_000), (40, 2, 9_000), (1560, 2, 20_000), (573, 8, 100_000)])
+def test_a_split_call_needs_its_workspace(n_q, heads, capacity):
+    """Few rows and tiles; the bytes do not shrink with the bound on the lengths
+    being given up (0: the capacity), and too few are refused."""
+    lib = L.lib()
+    c = cache(capacity=capacity, batch_stride=capacity, batch=1)
+    kw = dict(n_q=n_q, q_batch_stride=n_q, o_batch_stride=n_q, n_heads=heads)
+    need = L.cosmot_kv8_attention_workspace(c, query(**kw))
+    assert need > 0 and need >= L.cosmot_kv8_attention_workspace(c, query(**kw, max_len=64))
+    assert L.cosmot_kv8_attention_workspace(c, query(**kw, max_len=capacity)) == need
+    assert L.cosmot_kv8_attention_workspace(c, query(**kw, max_len=2 ** 31 - 1)) == need
+    ld = heads * 128
+    args = (ctypes.byref(c), ctypes.byref(query(**kw)), 256, ld, 256, ld, None)
+    assert lib.cosmot_kv8_attention(*args, None, need, None) == L.COSMOT_ERR_INVALID_ARG
+    assert lib.cosmot_kv8_attention(*args, 256, need - 1, None) == L.COSMOT_ERR_WORKSPACE
+    assert L.cosmot_kv8_attention_workspace(c, query(**{**kw, "n_q": 0})) == 0
+
+
 def test_the_python_layer_refuses_cpu_tensors_and_bad_layouts():
     t = torch.zeros((1, 16, 1, 64), dtype=torch.uint8).view(torch.float8_e4m3fn)
     s = torch.ones((1, 1, 1))
