@@ -297,8 +297,10 @@ __global__ void __launch_bounds__(kSelectThreads)
 // of a turn and of the ones after it before it writes the turn's blocks, and no
 // later source is a block that it has written, so the move is in place without any thread waiting
 // for another.  The pieces wait in the thread's own slots of shared memory.
-// 24 pieces on their way take 49 us where 16 take 59 and 8 take 62.
-constexpr int kMoveThreads = 128, kMoveTurn = 2, kMoveRing = 24;
+// 24 pieces on their way take 49 us where 16 take 59 and 8 take 62.  Eight blocks
+// a turn count where few threads walk far: 20,000 rows in blocks of 16, 2 heads
+// of 64, 600 kept: 70 us, with two a turn 89-94, with twelve 79.
+constexpr int kMoveThreads = 128, kMoveTurn = 8, kMoveRing = 24;
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ Cache c,
                                                                   const EvictPlan* plan,
