@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
       umma_commit_if(leader, bar_o_done);
-      warp_wait(bar_o_done, 0, p.status, kWhereKv8Drain);
+      mbar_drain(bar_o_done, 0, p.status, kWhereKv8Drain);
     }
     __syncwarp();
     } else {
@@ -801,11 +801,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       if (ranks > 1) cluster_sync();
     }
     // every copy lands before the CTA may exit
-    for (int i = n > kQSlots ? n - kQSlots : 0; i < n; ++i) {
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(bar_q_full + 8 * (i % kQSlots), (i / kQSlots) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {
-      }
-    }
+    for (int i = n > kQSlots ? n - kQSlots : 0; i < n; ++i)
+      mbar_drain(bar_q_full + 8 * (i % kQSlots), (i / kQSlots) & 1, p.status, kWhereKv8Drain);
     __syncwarp();
   } else if (warp == 1) {
     const uint32_t leader = elect_one();
@@ -838,7 +835,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       if (ranks > 1) cluster_sync();
     }
     umma_commit_if(leader, bar_done);
-    warp_wait(bar_done, 0, p.status, kWhereKv8Drain);
+    mbar_drain(bar_done, 0, p.status, kWhereKv8Drain);
+    __syncwarp();
   } else {
     // keys to bf16 (exact), rows behind the end zero; the warps take four (hd 64: eight) rows in turn
     constexpr int kRows = HD == 128 ? 4 : 8, kStep = kWeighConvWarps * kRows, kAhead = 6;

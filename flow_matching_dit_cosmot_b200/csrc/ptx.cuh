@@ -125,6 +125,21 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* st
   }
 }
 
+// The last wait for a CTA's own copies and products in flight, before its
+// shared and tensor memory go away: bounded too, but it does not give up for a
+// failure that something else has latched, since what is in flight goes on
+// writing.
+__device__ __forceinline__ bool mbar_drain(uint32_t bar, uint32_t parity, int* status, int where) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      latch_status(status, COSMOT_ERR_TIMEOUT, where);
+      return false;
+    }
+  }
+  return true;
+}
+
 // --------------------------------------------------------------------------
 // TMA (tensor maps are passed as __grid_constant__ kernel parameters)
 // --------------------------------------------------------------------------
