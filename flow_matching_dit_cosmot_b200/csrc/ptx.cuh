@@ -215,7 +215,10 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 }
 // Every thread of both CTAs; orders each CTA's earlier shared-memory writes
 // (barrier initialisation included) before the other CTA's later accesses.
+// (.aligned: the warp must be converged, which code behind a lane's branch does
+// not promise by itself)
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Shared::cluster address of the same shared-memory offset in CTA `rank`.

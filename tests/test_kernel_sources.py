@@ -24,3 +24,14 @@ def test_no_drain_gives_up_for_a_failure_of_others(name):
     """The wait for a CTA's own copies and products in flight ends when they have landed or after its time limit,
     never because the status word holds something: mbar_wait (and warp_wait over it) returns at once then."""
     assert not re.search(r"\b(mbar_wait|warp_wait)\([^;]*Drain\)", source(name))
+
+
+def test_warps_converge_before_an_aligned_cluster_barrier():
+    """barrier.cluster .aligned wants every lane of the warp at the same instruction; it is issued from one place, which
+    brings them together first."""
+    with open(os.path.join(CSRC, "ptx.cuh"), encoding="utf-8") as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    assert text.count("barrier.cluster.arrive") == 1
+    assert re.search(r"void cluster_sync\(\) \{\s*__syncwarp\(\);\s*asm volatile\(\s*\"barrier\.cluster\.arrive", text)
+    for name in FILES:
+        assert "barrier.cluster" not in source(name)
