@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kStoreThreads, kUnits <= 4 ? 6 : 4)
   const int32_t bg = side >> 1, b = bg / c.n_kv, g = bg % c.n_kv;
   const int32_t held = c.lens[b];
   if (held < 0 || held > c.capacity - n) {
-    if (threadIdx.x == 0) latch_status(status, COSMOT_ERR_BOUNDS, kWhereKv8Lens);
+    if (threadIdx.x == 0) report_status(status, COSMOT_ERR_BOUNDS, kWhereKv8Lens);
     return;
   }
   const int32_t blk = held / c.block + (int32_t)(blockIdx.x / sides);

@@ -62,11 +62,11 @@ __device__ __forceinline__ T load_global(const T* p) {
 }
 
 // Rows that sequence b shows: lens[b] + n_new, held inside the cache whatever
-// the device array says (a value outside latches COSMOT_ERR_BOUNDS).
+// the device array says (a value outside reports COSMOT_ERR_BOUNDS).
 __device__ __forceinline__ int32_t shown_rows(const Cache& c, int32_t b, int32_t n_new, int* status, bool report) {
   const int32_t held = c.lens[b];
   if (held >= 0 && held <= c.capacity - n_new) return held + n_new;
-  if (report) latch_status(status, COSMOT_ERR_BOUNDS, kWhereKv8Lens);
+  if (report) report_status(status, COSMOT_ERR_BOUNDS, kWhereKv8Lens);
   return held < 0 ? 0 : c.capacity;
 }
 

@@ -17,10 +17,16 @@ namespace cosmot {
 
 // --------------------------------------------------------------------------
 // Device status word (see cosmot_get_device_status): status[0] = first failure
-// code, status[1] = its site.  Kernels receive a pointer to it.
+// code, status[1] = its site.  Kernels receive a pointer to it.  status[2] and
+// status[3] hold the first report about a caller's data in the same form: it
+// ends no wait, so that one sequence's bad length costs no other its results.
 // --------------------------------------------------------------------------
 __device__ __forceinline__ void latch_status(int* status, int code, int where) {
   if (atomicCAS(status, 0, code) == 0) atomicExch(status + 1, where);
+}
+
+__device__ __forceinline__ void report_status(int* status, int code, int where) {
+  latch_status(status + 2, code, where);
 }
 
 __device__ __forceinline__ bool device_failed(const int* status) {

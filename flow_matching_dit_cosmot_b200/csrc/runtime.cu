@@ -9,7 +9,7 @@
 
 namespace cosmot {
 
-__device__ int g_status_word[2];
+__device__ int g_status_word[4];  // (code, site) of the first failure, then of the first report about a caller's data
 
 namespace {
 
@@ -165,16 +165,17 @@ cosmot_status cosmot_get_device_status(cosmot_stream_t stream, cosmot_status* ou
   if (!out) return COSMOT_ERR_INVALID_ARG;
   int* p = cosmot::device_status_ptr();
   if (!p) return COSMOT_ERR_CUDA;
-  int host[2] = {0, 0};
+  int host[4] = {0, 0, 0, 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cudaMemcpyAsync(host, p, sizeof(host), cudaMemcpyDeviceToHost, s) != cudaSuccess) return COSMOT_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return COSMOT_ERR_CUDA;
-  if (host[0] != 0) {
-    if (cudaMemsetAsync(p, 0, sizeof(host), s) != cudaSuccess) return COSMOT_ERR_CUDA;
+  const int at = host[0] != 0 ? 0 : 2;  // a failure first; a report behind it stays for the next call
+  if (host[at] != 0) {
+    if (cudaMemsetAsync(p + at, 0, 2 * sizeof(int), s) != cudaSuccess) return COSMOT_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return COSMOT_ERR_CUDA;
   }
-  *out = host[0];
-  if (where_out) *where_out = host[1];
+  *out = host[at];
+  if (where_out) *where_out = host[at + 1];
   return COSMOT_OK;
 }
 

@@ -71,6 +71,9 @@ COSMOT_API int32_t cosmot_version(void);
  * Reads the device status word on `stream` (synchronising that stream) into *out
  * and clears it.  COSMOT_OK if no kernel recorded a failure since the last call.
  * `where_out` (may be NULL) receives an internal site code of the first failure.
+ * A length of an 8-bit cache outside its capacity (COSMOT_ERR_BOUNDS) is kept
+ * apart: it stops no kernel, and where there is a failure too it is what the
+ * next call reads.
  */
 COSMOT_API cosmot_status cosmot_get_device_status(cosmot_stream_t stream, cosmot_status* out, int32_t* where_out);
 
@@ -376,10 +379,11 @@ COSMOT_API cosmot_status cosmot_flow_cfg_euler_step(void* x_cond, void* x_base, 
  *            cosmot_kv8_store writes)
  *   lens     device int32 [batch]: rows that each sequence holds, [0, capacity].
  *            The kernels read it, so a captured graph follows it.  A value
- *            outside (or without room for the rows of the call) latches
- *            COSMOT_ERR_BOUNDS; nothing is read or written out of place: a store
- *            then writes none of that sequence's rows, the other calls take the
- *            nearest length inside.
+ *            outside (or without room for the rows of the call) is reported as
+ *            COSMOT_ERR_BOUNDS by cosmot_get_device_status; nothing is read or
+ *            written out of place: a store then writes none of that sequence's
+ *            rows, the other calls take the nearest length inside.  Other
+ *            sequences and other calls are as if it were not there.
  * head_dim 64 or 128, block 16, 32, 64 or 128 (else UNSUPPORTED); any capacity.
  * Contents of rows at and behind lens (+ n_new) are never read.
  */

@@ -35,3 +35,69 @@ def test_calls_after_a_failure_end_and_the_next_ones_are_right():
     assert torch.equal(o, want) and torch.equal(lse, wl)
     assert torch.equal(c.weigh(q, lse, c.empty_weight()), w)
     assert_device_ok()
+
+
+# ------------------------------------------------------------------ a length outside the cache
+
+def _status():
+    return L.cosmot_get_device_status(torch.cuda.current_stream().cuda_stream)
+
+
+@pytest.mark.parametrize("n", [1, 40, 150, 260])
+@pytest.mark.parametrize("bad,nearest", [(-3, 0), (401, 400), (2 ** 31 - 1, 400), (-2 ** 31, 0)])
+def test_a_bad_length_costs_no_other_sequence_its_results(n, bad, nearest):
+    """The sequence takes the nearest length inside; the others' outputs, weights and blocks are the good batch's."""
+    lens = [nearest, 333, 400]
+    good = scattered(3, 400, 2, 128, 32, lens, seed=210)
+    c = scattered(3, 400, 2, 128, 32, [bad, 333, 400], seed=210)
+    q = queries(211, 3, n, 8, 128) * 0.2
+    want, wl = good.attend(q)
+    ww = good.weigh(q, wl, good.empty_weight())
+    assert_device_ok()
+    o, lse = c.attend(q)
+    w = c.weigh(q, lse, c.empty_weight())
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, wl) and torch.equal(w, ww)
+    good.evict(ww, 5)
+    c.evict(w, 5)
+    torch.cuda.synchronize()
+    assert torch.equal(w, ww) and torch.equal(c.lens, good.lens)
+    assert torch.equal(c.k.view(torch.uint8), good.k.view(torch.uint8))
+    assert _status() == (L.COSMOT_ERR_BOUNDS, 400)
+    assert_device_ok()
+
+
+def test_a_store_without_room_costs_other_calls_nothing():
+    """The report stays unread while the layer's products and bf16 attention and this cache's own calls run."""
+    from test_gpu_layer import MEDIUM, LayerRun
+    import synth
+    from gpu_helpers import to_dev
+    run = LayerRun(MEDIUM, synth.preset("droid").layout)
+    first, again = to_dev(run.h), to_dev(run.h)
+    out, out2 = torch.empty_like(first), torch.empty_like(first)
+    run.layer.forward(first, out, 0.8, 0.7, run.seq)
+    assert_device_ok()
+    c = scattered(2, 300, 2, 64, 16, [296, 100], seed=212)
+    before = c.k.view(torch.uint8).clone()
+    x = rows(214, 2, 8, 2, 64)
+    c.store(x, x)  # sequence 0 has no room for 8 rows
+    run.layer.forward(again, out2, 0.8, 0.7, run.seq)
+    c.lens.copy_(torch.tensor([296, 108], dtype=torch.int32))
+    q = queries(213, 2, 200, 4, 64) * 0.2
+    o, lse = c.attend(q)
+    torch.cuda.synchronize()
+    assert torch.equal(again, first) and torch.equal(out2, out)
+    assert torch.equal(c.k.view(torch.uint8)[0], before[0])
+    assert _status() == (L.COSMOT_ERR_BOUNDS, 400)
+    o2, lse2 = check_attend(c, q, [296, 108], False)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_a_failure_is_read_before_a_report_and_neither_is_lost():
+    c = scattered(1, 64, 1, 64, 16, [64], seed=220)
+    x = rows(221, 1, 1, 1, 64)
+    c.store(x, x)
+    L.cosmot_selftest_wait_timeout(torch.cuda.current_stream().cuda_stream)
+    assert _status() == (L.COSMOT_ERR_TIMEOUT, L.COSMOT_SITE_SELFTEST)
+    assert _status() == (L.COSMOT_ERR_BOUNDS, 400)
+    assert_device_ok()
