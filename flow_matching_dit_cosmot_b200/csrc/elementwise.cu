@@ -54,7 +54,7 @@ __device__ __forceinline__ void load8_f32(const float* p, float* f) {
 }
 
 template <int kVecPerLane>
-__global__ void __launch_bounds__(256) rmsnorm_f32in_kernel(const float* __restrict__ h, int64_t ld_h,
+__global__ void __launch_bounds__(256) rmsnorm_f32in_kernel(const float* h, int64_t ld_h,
                                                             const SegTable segs, const __nv_bfloat16* __restrict__ g0,
                                                             const __nv_bfloat16* __restrict__ g1, int32_t d, float eps,
                                                             __nv_bfloat16* __restrict__ out, int64_t ld_out,
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(256) rmsnorm_f32in_kernel(const float* __restr
 constexpr int kNormBlock = 128;
 
 template <typename TIn, int kVecPerThread>
-__global__ void __launch_bounds__(kNormBlock) rmsnorm_block_kernel(const TIn* __restrict__ h, int64_t ld_h,
+__global__ void __launch_bounds__(kNormBlock) rmsnorm_block_kernel(const TIn* h, int64_t ld_h,
                                                                   const SegTable segs,
                                                                   const __nv_bfloat16* __restrict__ g0,
                                                                   const __nv_bfloat16* __restrict__ g1, int32_t d,
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kNormBlock) rmsnorm_block_kernel(const TIn* __
 }
 
 template <int kVecPerLane>
-__global__ void __launch_bounds__(256) rmsnorm_kernel(const __nv_bfloat16* __restrict__ h, int64_t ld_h,
+__global__ void __launch_bounds__(256) rmsnorm_kernel(const __nv_bfloat16* h, int64_t ld_h,
                                                       const SegTable segs, const __nv_bfloat16* __restrict__ g0,
                                                       const __nv_bfloat16* __restrict__ g1, int32_t d, float eps,
                                                       __nv_bfloat16* __restrict__ out, int64_t ld_out,
@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(256) rmsnorm_kernel(const __nv_bfloat16* __res
 // ---------------------------------------------------------------- mRoPE
 // One thread per (row, head, group of 8 pairs): reads x[i..i+7] and
 // x[i+hd/2..+7], rotates them with the table and writes both back.
-__global__ void __launch_bounds__(256) mrope_kernel(__nv_bfloat16* __restrict__ q, int64_t ld_q, int32_t n_q_heads,
-                                                    __nv_bfloat16* __restrict__ k, int64_t ld_k, int32_t n_k_heads,
+__global__ void __launch_bounds__(256) mrope_kernel(__nv_bfloat16* q, int64_t ld_q, int32_t n_q_heads,
+                                                    __nv_bfloat16* k, int64_t ld_k, int32_t n_k_heads,
                                                     int64_t n_rows, int32_t head_dim,
                                                     const float2* __restrict__ cs) {
   pdl_trigger();
@@ -305,8 +305,8 @@ __global__ void __launch_bounds__(256) mrope_kernel(__nv_bfloat16* __restrict__ 
 }
 
 // ---------------------------------------------------------------- Euler
-__global__ void __launch_bounds__(256) euler_kernel(__nv_bfloat16* __restrict__ x, int64_t ld_x,
-                                                    const __nv_bfloat16* __restrict__ v, int64_t ld_v,
+__global__ void __launch_bounds__(256) euler_kernel(__nv_bfloat16* x, int64_t ld_x,
+                                                    const __nv_bfloat16* v, int64_t ld_v,
                                                     int64_t row_begin, int64_t n_rows, int64_t n_cols, float dsigma,
                                                     int* status) {
   pdl_trigger();
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(256) euler_kernel(__nv_bfloat16* __restrict__ 
     if (!dcheck(r < row_begin + n_rows && c + 8 <= n_cols, status, kWhereEulerStore)) continue;
     uint4* xp = reinterpret_cast<uint4*>(x + r * ld_x + c);
     uint4 xv = *xp;
-    uint4 vv = __ldg(reinterpret_cast<const uint4*>(v + r * ld_v + c));
+    uint4 vv = load_global(reinterpret_cast<const uint4*>(v + r * ld_v + c));
     uint32_t* xu = reinterpret_cast<uint32_t*>(&xv);
     const uint32_t* vu = reinterpret_cast<const uint32_t*>(&vv);
 #pragma unroll
@@ -337,8 +337,8 @@ __global__ void __launch_bounds__(256) euler_kernel(__nv_bfloat16* __restrict__ 
 // a (conditioned, baseline) pair so they stay identical for the next step.
 __global__ void __launch_bounds__(256) cfg_euler_kernel(__nv_bfloat16* x_cond, __nv_bfloat16* x_base,
                                                         int64_t ld_x,
-                                                        const __nv_bfloat16* __restrict__ v_cond,
-                                                        const __nv_bfloat16* __restrict__ v_base, int64_t ld_v,
+                                                        const __nv_bfloat16* v_cond,
+                                                        const __nv_bfloat16* v_base, int64_t ld_v,
                                                         int64_t n_rows, int64_t n_cols, float dsigma, float w) {
   pdl_trigger();
   pdl_wait();
@@ -348,8 +348,8 @@ __global__ void __launch_bounds__(256) cfg_euler_kernel(__nv_bfloat16* x_cond, _
     const int64_t r = e / vec_per_row;
     const int64_t c = (e % vec_per_row) << 3;
     uint4 xv = *reinterpret_cast<const uint4*>(x_cond + r * ld_x + c);
-    const uint4 vc = __ldg(reinterpret_cast<const uint4*>(v_cond + r * ld_v + c));
-    const uint4 vb = __ldg(reinterpret_cast<const uint4*>(v_base + r * ld_v + c));
+    const uint4 vc = load_global(reinterpret_cast<const uint4*>(v_cond + r * ld_v + c));
+    const uint4 vb = load_global(reinterpret_cast<const uint4*>(v_base + r * ld_v + c));
     uint32_t* xu = reinterpret_cast<uint32_t*>(&xv);
     const uint32_t* cu = reinterpret_cast<const uint32_t*>(&vc);
     const uint32_t* bu = reinterpret_cast<const uint32_t*>(&vb);

@@ -53,14 +53,6 @@ struct Query {
   int* status;
 };
 
-// A load that stays behind griddepcontrol.wait.  __ldg and const __restrict__
-// promise that nobody writes the memory while the kernel lives, so the compiler
-// may lift them above that wait, where the previous kernel still writes.
-template <typename T>
-__device__ __forceinline__ T load_global(const T* p) {
-  return *p;
-}
-
 // Rows that sequence b shows: lens[b] + n_new, held inside the cache whatever
 // the device array says (a value outside reports COSMOT_ERR_BOUNDS).
 __device__ __forceinline__ int32_t shown_rows(const Cache& c, int32_t b, int32_t n_new, int* status, bool report) {

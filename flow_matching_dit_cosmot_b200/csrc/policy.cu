@@ -54,7 +54,7 @@ __device__ __forceinline__ int seg_of(const ActSegs& s, int64_t r) {
 }
 
 // h[out] = bf16(x[row] . W_in^T): thread (row, 8-column chunk).
-__global__ void __launch_bounds__(256) action_embed_kernel(const __nv_bfloat16* __restrict__ x, int64_t ld_x,
+__global__ void __launch_bounds__(256) action_embed_kernel(const __nv_bfloat16* x, int64_t ld_x,
                                                            const ActSegs segs,
                                                            const __nv_bfloat16* __restrict__ w_in, int32_t ca,
                                                            int32_t d, __nv_bfloat16* __restrict__ h, int64_t ld_h) {
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(256) action_embed_kernel(const __nv_bfloat16* 
 // Velocity of one action row in one pass: lane c (< ca) returns
 // v_c = rstd * sum_j h_j g_j w_out[c, j] (the RMS scale factored out of the
 // sums), fp32 throughout; 16-byte loads of h, g and each W_out row.
-__device__ __forceinline__ float action_velocity_row(const __nv_bfloat16* __restrict__ hr,
+__device__ __forceinline__ float action_velocity_row(const __nv_bfloat16* hr,
                                                      const __nv_bfloat16* __restrict__ g,
                                                      const __nv_bfloat16* __restrict__ w_out, int32_t ca, int32_t d,
                                                      float eps, int lane) {
@@ -95,7 +95,7 @@ __device__ __forceinline__ float action_velocity_row(const __nv_bfloat16* __rest
   for (int c = 0; c < kMaxActionDim; ++c) acc[c] = 0.f;
   float ss = 0.f;
   for (int j8 = lane * 8; j8 < d; j8 += 256) {
-    const uint4 hv = __ldg(reinterpret_cast<const uint4*>(hr + j8));
+    const uint4 hv = load_global(reinterpret_cast<const uint4*>(hr + j8));
     const uint4 gv = __ldg(reinterpret_cast<const uint4*>(g + j8));
     const uint32_t* hu = reinterpret_cast<const uint32_t*>(&hv);
     const uint32_t* gu = reinterpret_cast<const uint32_t*>(&gv);
@@ -139,7 +139,7 @@ __device__ __forceinline__ float action_velocity_row(const __nv_bfloat16* __rest
 
 // One warp per action row (unguided) or per conditioned/baseline pair of rows
 // (guided: segments 2p and 2p+1 are the pair).  x[out] = bf16(x[out] + dsigma v).
-__global__ void __launch_bounds__(256) action_head_kernel(const __nv_bfloat16* __restrict__ h, int64_t ld_h,
+__global__ void __launch_bounds__(256) action_head_kernel(const __nv_bfloat16* h, int64_t ld_h,
                                                           const ActSegs segs, const __nv_bfloat16* __restrict__ g,
                                                           float eps, const __nv_bfloat16* __restrict__ w_out,
                                                           int32_t ca, int32_t d, __nv_bfloat16* x, int64_t ld_x,

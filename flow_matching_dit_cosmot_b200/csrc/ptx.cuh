@@ -47,6 +47,16 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A load that stays behind pdl_wait.  __ldg and __restrict__ on what a kernel
+// reads promise that nobody writes the memory while the kernel lives, so the
+// compiler may lift the load above that wait, where the previous kernel still
+// writes.  They are for what no kernel that triggers early writes (gains and
+// weights, tables); `out` pointers that are only written may be __restrict__.
+template <typename T>
+__device__ __forceinline__ T load_global(const T* p) {
+  return *p;
+}
+
 __device__ __forceinline__ uint64_t globaltimer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));

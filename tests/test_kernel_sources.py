@@ -35,3 +35,28 @@ def test_warps_converge_before_an_aligned_cluster_barrier():
     assert re.search(r"void cluster_sync\(\) \{\s*__syncwarp\(\);\s*asm volatile\(\s*\"barrier\.cluster\.arrive", text)
     for name in FILES:
         assert "barrier.cluster" not in source(name)
+
+
+# What kernels that are launched early may hold to be constant while they live: weights, and the tables that only
+# kernels which never trigger their successor write.
+CONSTANTS = {"g", "g0", "g1", "gv", "w_in", "w_out", "cs", "cs_row", "t", "p.chunk"}
+WRITTEN_ONLY = {"rmsnorm_f32in_kernel": "out", "rmsnorm_block_kernel": "out", "rmsnorm_kernel": "out", "action_embed_kernel": "h"}
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_no_load_of_an_earlier_kernels_output_may_pass_the_wait_for_it(name):
+    """__ldg and __restrict__ let the compiler lift a load above griddepcontrol.wait, where the kernel before still
+    writes.  Kernels without that wait may use them."""
+    text = re.sub(r"__launch_bounds__\((?:[^()]|\([^()]*\))*\)", "", source(name))
+    for m in re.finditer(r"__ldg\((?:reinterpret_cast<[^>]*>\()?\s*([\w.]+)", text):
+        assert m.group(1) in CONSTANTS, f"__ldg of {m.group(1)}"
+    heads = list(re.finditer(r"(?:__global__|__device__ __forceinline__)[^;{(]*?(\w+)\(([^{;]*)\)\s*\{", text))
+    waits = {m.group(1): "pdl_wait();" in text[m.end():m.end() + 1600] for m in heads}
+    for m in heads:
+        if not waits[m.group(1)] and m.group(0).startswith("__global__"):
+            continue
+        for const, var in re.findall(r"(const )?\w+\s*\*\s*__restrict__\s+(\w+)", m.group(2)):
+            if const:
+                assert var in CONSTANTS, f"{m.group(1)}: {var} is read"
+            else:
+                assert WRITTEN_ONLY.get(m.group(1)) == var, f"{m.group(1)}: {var} may be read"
