@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
           float t = i ? t1 : t0;
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
-          const float to = fmaxf(m[n][i], t);
+          const float to = t > m[n][i] + kFollow ? t : m[n][i];  // a row of its own: whatever the others do
           const float corr = to == m[n][i] ? 1.f : ex2_approx(m[n][i] - to);  // 0 from -inf
           m[n][i] = to;
           l[n][i] *= corr;

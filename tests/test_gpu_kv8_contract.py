@@ -101,3 +101,20 @@ def test_a_failure_is_read_before_a_report_and_neither_is_lost():
     assert _status() == (L.COSMOT_ERR_TIMEOUT, L.COSMOT_SITE_SELFTEST)
     assert _status() == (L.COSMOT_ERR_BOUNDS, 400)
     assert_device_ok()
+
+
+# ------------------------------------------------------------------ rows apart, value scales far apart
+
+@pytest.mark.parametrize("n", [3, 8, 60, 300])
+def test_a_row_does_not_depend_on_the_rows_beside_it(n):
+    """Keys that grow along the cache: a row's maximum moves many times, at its own keys whatever the others do."""
+    c = scattered(1, 1300, 1, 64, 16, [1300], seed=240)
+    c.k_scale.copy_(2.0 ** torch.linspace(-12, -3, c.n_blocks, device="cuda").floor())
+    q = queries(241, 1, n, 2, 64)
+    q[:, ::2] *= 0.25
+    o, lse = c.attend(q)
+    alone = q.clone()
+    alone[:, 1::2] = 0
+    oa, la = c.attend(alone)
+    assert torch.equal(o[:, ::2], oa[:, ::2]) and torch.equal(lse[:, :, ::2], la[:, :, ::2])
+    check_attend(c, q, [1300], False)
