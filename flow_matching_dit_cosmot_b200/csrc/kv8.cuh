@@ -6,9 +6,10 @@
 // on the float32 side: a key block's scale multiplies its scores, and a value
 // block's scale is added to the exponent of its softmax weights,
 //     p vs = 2^(x - m + log2 vs),   sum p = sum (p vs) / vs,
-// so that no element needs a multiplication of its own.  The running maximum
-// m is over x + log2 vs.  The store writes powers of two in [2^-40, 2^40]; the
-// spread of the exponents keeps every sum inside float32.
+// so that no element needs a multiplication of its own.  P is f16 or bf16 for the
+// tensor cores: each kernel says how it keeps the spread of the scales out of
+// their range.  The store writes powers of two in [2^-40, 2^40]; with those every
+// sum stays inside float32.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -92,6 +93,11 @@ __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
 }
 
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+// 2^x of a whole x in [-126, 127] held as a float.
+__device__ __forceinline__ float exp2_whole(float x) {
+  return __int_as_float(__float_as_int(x + (12582912.f + 127.f)) << 23);  // 1.5 * 2^23: the sum's low bits are x + 127
+}
 
 // log2 of a positive scale and the factor 2^-log2, both exact for a power of two.
 __device__ __forceinline__ void scale_log2_parts(float s, float& log2s, float& inv) {

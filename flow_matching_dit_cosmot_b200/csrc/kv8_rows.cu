@@ -17,9 +17,19 @@
 // of cp.async stages in shared memory that no other lane reads, with no
 // barrier, and leave the registers to the products.
 // Q (bf16) becomes f16 by a power of two per row that puts its largest
-// magnitude in [2^13, 2^14): exact down to 2^-31 of it.  P (f16) is kept times
-// 2^8, and the running maximum follows only when it grows by more than 2^7:
-// full precision for weights down to 2^-22 of the largest.
+// magnitude in [2^13, 2^14): exact down to 2^-31 of it.
+// P (f16) is 2^11 times the weight relative to the running maximum of the
+// scores, which follows only when it grows by more than 2^4, times the block's
+// value scale in units of 2^v_exp, at most 1 and more than 2^-3: below 2^15, full
+// precision for weights down to 2^-22 of the largest, and a step of 2^-32 of it
+// below.  O^T is in those units too.  A block whose scale lies outside the window
+// moves it: the accumulators change by a power of two, which float32 holds
+// exactly, so that scales far apart cost the weights no digits.  (The window costs
+// 0.5 % for one token and 4 % at 32 rows x 32 heads; with every scale in the
+// exponent, whatever their spread, small ones lose their digits.  A window of one power took 10 % more where
+// neighbouring blocks differ by one; to bring every 16 keys' share in by its own
+// scale 2 % and 12 %; to follow the maximum at 2^7 saves 1.5 % and costs three
+// digits.)
 #include "kv8.cuh"
 
 #include <mutex>
@@ -31,7 +41,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kRing = 3;  // stages of 16 keys
 constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : 3; }  // shared memory and registers allow
-constexpr float kPBias = 8.f, kFollow = 7.f;
+constexpr float kPBias = 11.f, kFollow = 4.f, kVWindow = 2.f;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -202,7 +212,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
   const float* ksp = c.k_scale + (int64_t)blockIdx.z * c.n_blocks;
   const float* vsp = c.v_scale + (int64_t)blockIdx.z * c.n_blocks;
   const int block_shift = 31 - __clz(c.block);
-  float4* scales = reinterpret_cast<float4*>(sm_raw);  // (ks, log2 vs, 1/vs)
+  float4* scales = reinterpret_cast<float4*>(sm_raw);  // (ks, log2 vs, 1/vs, log2 vs rounded up)
   const uint32_t ring = smem_u32(sm_raw) + R::kScales * 16 + warp * kRing * R::kStage;
   // V pieces: a row's eight pieces side by side, turned by the row so that the
   // lanes' reads fall on all banks too
@@ -237,7 +247,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
     float4 s;
     s.x = load_global(ksp + blk);
     scale_log2_parts(load_global(vsp + blk), s.y, s.z);
-    s.w = 0.f;
+    s.w = ceilf(s.y);
     return s;
   };
   const int32_t blk0 = k0 >> block_shift, blk1 = ((kend - 1) >> block_shift) + 1;
@@ -262,7 +272,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
   constexpr int kTiles = HD / 16;  // row tiles of O^T
   constexpr int VW = HD / 32;      // 32-bit words of a V piece
   float o[NT][kTiles][4];
-  float m[NT][2], l[NT][2];
+  float m[NT][2], l[NT][2], v_exp = 0.f;  // o is in units of 2^v_exp
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -287,7 +297,13 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
     }
     const int32_t blk = key0 >> block_shift;
     const float4 sc = blk - blk0 < R::kScales ? scales[blk - blk0] : scale_of(blk);
-    const float ks = sc.x, vlog = sc.y, vinv = sc.z;
+    const float ks = sc.x;
+    // (the warp's 16 keys have one value scale)
+    const bool moved = sc.w > v_exp || sc.w < v_exp - kVWindow;
+    const float v_by = moved ? v_exp - sc.w : 0.f;
+    v_exp = moved ? sc.w : v_exp;
+    // the scale's log2 in units of 2^v_exp, in (-kVWindow - 1, 0], and 2^-it
+    const float p_bias = kPBias + (sc.y - v_exp), v_inv = sc.z * exp2_whole(v_exp);
 
     float s[NT][4];
     scores<HD, NT>(s, ka, kc, q);
@@ -298,8 +314,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float f = fac[n][i] * ks;
-        s[n][i] = fmaf(s[n][i], f, vlog);
-        s[n][2 + i] = fmaf(s[n][2 + i], f, vlog);
+        s[n][i] *= f;
+        s[n][2 + i] *= f;
       }
       if (key0 + 16 > lim_min) {
 #pragma unroll
@@ -309,8 +325,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
         }
       }
       const float t0 = fmaxf(s[n][0], s[n][2]), t1 = fmaxf(s[n][1], s[n][3]);
-      // (-inf > -inf + 7 is false: a row that has seen nothing stays where it is)
-      if (__any_sync(0xffffffffu, t0 > m[n][0] + kFollow || t1 > m[n][1] + kFollow)) {
+      // (-inf > -inf + 4 is false: a row that has seen nothing stays where it is)
+      if (__any_sync(0xffffffffu, moved || t0 > m[n][0] + kFollow || t1 > m[n][1] + kFollow)) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float t = i ? t1 : t0;
@@ -320,20 +336,21 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
           const float corr = to == m[n][i] ? 1.f : ex2_approx(m[n][i] - to);  // 0 from -inf
           m[n][i] = to;
           l[n][i] *= corr;
+          const float o_by = corr * exp2_whole(fminf(fmaxf(v_by, -126.f), 126.f));
 #pragma unroll
           for (int d = 0; d < kTiles; ++d) {
-            o[n][d][i] *= corr;
-            o[n][d][2 + i] *= corr;
+            o[n][d][i] *= o_by;
+            o[n][d][2 + i] *= o_by;
           }
         }
       }
       float pr[4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float mu = m[n][i] == -INFINITY ? 0.f : m[n][i] - kPBias;
+        const float mu = m[n][i] == -INFINITY ? 0.f : m[n][i] - p_bias;
         pr[i] = ex2_approx(s[n][i] - mu);
         pr[2 + i] = ex2_approx(s[n][2 + i] - mu);
-        l[n][i] = fmaf(pr[i] + pr[2 + i], vinv, l[n][i]);
+        l[n][i] = fmaf(pr[i] + pr[2 + i], v_inv, l[n][i]);
       }
       pb[n][0] = transpose8x8(pack_f16x2(pr[0], pr[1]));
       pb[n][1] = transpose8x8(pack_f16x2(pr[2], pr[3]));
@@ -362,6 +379,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
       }
     }
   }
+  const float v_unit = exp2_whole(v_exp);
   cp_async_wait<0>();
   __syncthreads();  // the ring's memory takes the warps' parts now
 
@@ -379,7 +397,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
       if (g == 0) sm_ml[row] = make_float2(m[n][i], lr);
 #pragma unroll
       for (int d = 0; d < kTiles; ++d)
-        *reinterpret_cast<float2*>(sm_o + row * R::kRowPitch + g * (HD / 8) + 2 * d) = make_float2(o[n][d][i], o[n][d][2 + i]);
+        *reinterpret_cast<float2*>(sm_o + row * R::kRowPitch + g * (HD / 8) + 2 * d) = make_float2(o[n][d][i] * v_unit, o[n][d][2 + i] * v_unit);
     }
   __syncthreads();
   // a thread joins the warps' parts of 4 columns of a row, in warp order

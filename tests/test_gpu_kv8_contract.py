@@ -118,3 +118,23 @@ def test_a_row_does_not_depend_on_the_rows_beside_it(n):
     oa, la = c.attend(alone)
     assert torch.equal(o[:, ::2], oa[:, ::2]) and torch.equal(lse[:, :, ::2], la[:, :, ::2])
     check_attend(c, q, [1300], False)
+
+
+@pytest.mark.parametrize("n", [1, 3, 8])
+@pytest.mark.parametrize("large,small", [(20, -13), (40, -40), (3, -25), (-13, 20)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_a_large_scale_over_small_bytes_hides_no_other_value(n, large, small, causal):
+    """The bound is relative to the values, not to their blocks' scales: a block of a large scale whose rows are zero
+    (an outlier row that went, or that the mask hides) leaves the others' digits alone."""
+    lens = [400, 133]
+    c = filled(2, 400, 2, 128, 32, lens, seed=230)
+    c.v_scale[:, :, :12] = 2.0 ** small * torch.tensor([1.0, 2.0, 4.0] * 4, device="cuda")
+    c.v_scale[:, 0, 1::4] = 2.0 ** large
+    c.v_scale[:, 1, 0:12:3] = 2.0 ** large
+    for h, first, step in ((0, 1, 4), (1, 0, 3)):
+        for j in range(first, 12, step):
+            c.v.view(torch.uint8)[:, 32 * j:32 * j + 32, h] = 0
+    for b, m in enumerate(lens):  # nothing reads the scales of blocks without a row
+        c.v_scale[b, :, -(-m // 32):] = math.nan
+    q = queries(231, 2, n, 4, 128)
+    check_attend(c, q, lens, causal)
