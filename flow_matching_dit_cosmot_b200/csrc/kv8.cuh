@@ -123,6 +123,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // Key splits of a row: split s gives o_s = sum 2^(x - ref_s) v8 and (ref_s,
 // l_s) with l_s = sum 2^(x - ref_s) / vs; where a split shows the row nothing,
 // l_s = 0 and o_s is zero or was not written (each kernel says which).

@@ -16,14 +16,25 @@
 //                power of two per row (its largest magnitude in [2^13, 2^14):
 //                exact down to 2^-31 of it).
 // The scales of a 128-key tile come with its keys, one for each 128 / NG keys:
-//     x = s (q factor)(ks) + log2 vs,   p vs = 2^(x - m + 8)  (f16 in TMEM),
+//     x = s (q factor)(ks) + y,   p 2^y = 2^(x - m + 10)  (f16 in TMEM),
 // m the running maximum of x; it is followed only when it grows by more than
-// 2^7, so p vs stays below 2^15 and f16 keeps full precision down to 2^-22 of
-// the largest weight.  l = sum (p vs) / vs stays in float32.
+// 2^5, so p 2^y stays below 2^15.  l = sum (p 2^y) / 2^y stays in float32.
+// Where the value scales of a CTA's keys lie within 2^2 of one another (warp 0
+// looks at them all while the queries come in), y = log2 vs: f16 keeps full
+// precision down to 2^-22 of the largest weight, a step of 2^-32 of it below.
+// Otherwise vs = 2^(y + shift + unit) with -1 < y <= 0: V's tile is widened times
+// 2^shift, exact from 2^-15 to 2^7, and O is in units of 2^unit, which moves from
+// tile to tile so that the tile's scales fit (O changes by a power of two then,
+// like for a maximum that moved).  Only blocks of one tile further apart than
+// 2^22 leave a rest in y, and the smaller ones' weights lose digits by it.
+// 1,560 queries x 14,106 rows x 32 heads: 365 us with near scales, 380 with random
+// ones in 2^4, 427 in 2^40; 363 where any spread went into y, which is wrong for
+// far ones.  P as two bf16 where scales are far took 10 % more with near ones too
+// (the softmax's registers), the same shifts for every CTA 6 to 10 %.
 // bound: the chain S -> softmax -> PV of a query tile, two tiles half a period
 // apart: 3,340 cycles a key tile (2,800 without the exponentials; the products
-// alone 2,048).  1,560 queries x 14,106 rows x 32 heads: 362 us = 994 TFLOP/s,
-// 409 us in long runs under the power cap; tensor pipe and SFU at 50 %.
+// alone 2,048).  The same sizes: 409 us = 880 TFLOP/s in long runs under the power
+// cap, 365 us (986) on a cool card; tensor pipe and SFU at 50 %.
 // Registers a thread: 176 for the softmax and 80 for the other warps measured
 // best (184 / 72 +2 %, 192 / 64 +6 %, 168 / 88 the same).
 //
@@ -38,6 +49,7 @@
 // SFU 257 where a quarter off it took 233, three eighths 244.
 #include "kv8.cuh"
 
+#include <climits>
 #include <mutex>
 
 namespace cosmot {
@@ -47,8 +59,10 @@ namespace {
 constexpr int kTile = 128;                    // rows of a query tile, keys of a key tile
 constexpr int kSlots = 4;
 constexpr int kBoxBytes = 128 * 64 * 2;       // 128 rows x 64 columns of 16 bits, 128-byte swizzle
-constexpr float kTileBias = 8.f;
-constexpr float kFollow = 7.f;                // log2 units
+constexpr float kTileBias = 10.f;
+constexpr float kFollow = 5.f;                // log2 units
+constexpr float kFold = 2.f;                  // spread of the value scales' log2 that the weights' exponents take
+constexpr int kShiftLo = -15, kShiftHi = 7;   // powers of two by which e4m3 stays exact in f16
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -127,7 +141,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const uint32_t bar_p_full = bar_p_half + 16;            // [2] P of keys 64-127 written
   const uint32_t bar_o_done = bar_p_full + 16;            // [1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 1 + 2 * kSlots + 7);
-  // [4][NG] (ks, log2 vs, 1/vs)
+  const uint32_t bar_span = smem_u32(bars + 24);            // [1] vs_top is written
+  int32_t* vs_top = reinterpret_cast<int32_t*>(bars + 25);  // log2 of the largest value scale; INT_MIN: all are near
+  // [4][NG] (ks, y, 2^-y, unit)
   float4* scales = reinterpret_cast<float4*>(smem + (2 + kSlots) * C::kTileBytes + 256);
   constexpr int kGroupKeys = kTile / NG;
 
@@ -160,6 +176,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(bar_p_full + 8 * t, 4);
     }
     mbar_init(bar_o_done, 1);
+    mbar_init(bar_span, 1);
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -204,6 +221,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       };
       auto wait = [&](uint32_t bar, uint32_t par) { return warp_wait(bar, par, p.status, kWhereKv8Mma); };
       auto kv_wait = [&](int L) { return wait(bar_kv_full + 8 * (L % kSlots), (L / kSlots) & 1); };
+      {  // the value scales of this CTA's keys, mostly near one another
+        const float* vsp = c.v_scale + (int64_t)bg * c.n_blocks;
+        const int32_t end = min(kt1 * NG, (kend + kGroupKeys - 1) / kGroupKeys);
+        int hi = INT_MIN, lo = INT_MAX;  // positive floats order like their bits
+#pragma unroll 8
+        for (int32_t i = kt0 * NG + lane; i < end; i += 32) {
+          const int v = __float_as_int(load_global(vsp + i));
+          hi = max(hi, v);
+          lo = min(lo, v);
+        }
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        float top, low, inv;
+        scale_log2_parts(__int_as_float(hi), top, inv);
+        scale_log2_parts(__int_as_float(lo), low, inv);
+        if (lane == 0) {
+          *vs_top = top - low > kFold ? (int)ceilf(top) : INT_MIN;
+          mbar_arrive(bar_span);
+        }
+        __syncwarp();
+      }
       bool ok = wait(bar_q, 0) && kv_wait(0);
       if (ok) {
         tc_fence_after();
@@ -254,34 +292,60 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncwarp();
     } else {
     // ---------------------------------------------------------- widening
+    // The widening warps live on 80 registers: addresses that step along keep them
+    // from spilling in this loop, which costs up to 10 % where it paces the tile.
     // A warp takes 32 pieces of 16 bytes at a time, kRows whole rows; the tile's
     // row groups go round the seven warps.  Eight neighbouring lanes write two
     // rows' pieces of one box: their chunks of 16 bytes fall on all banks (four
     // pieces give every other chunk of a row).
     constexpr int kRows = HD == 128 ? 4 : 8, kRowGroups = kTile / kRows;
-    constexpr int kLoads = (kRowGroups + kConvWarps - 1) / kConvWarps;
+    constexpr int kLoads = (kRowGroups + kConvWarps - 1) / kConvWarps, kStep = kConvWarps * kRows;
     const int cw = warp - 1;
     const int u = HD == 128 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3;
     const int row = cw * kRows + (HD == 128 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane >> 2);
-    const uint8_t* kb = c.k + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD + u * 16;
-    const uint8_t* vb = c.v + (int64_t)b * c.bstride * c.ld + (int64_t)kvh * HD + u * 16;
+    const int64_t start = ((int64_t)b * c.bstride + (int64_t)kt0 * kTile + row) * c.ld + (int64_t)kvh * HD + u * 16;
+    const uint8_t* kp = c.k + start;  // this lane's first row of the next tile to load
+    const uint8_t* vp = c.v + start;
+    int32_t left_k = kend - kt0 * kTile - row, left_v = left_k;  // rows from there to the end
     uint4 wk[kLoads], wv[kLoads];
-    auto load = [&](uint4 (&w)[kLoads], const uint8_t* base, int32_t kt) {
+    auto load = [&](uint4 (&w)[kLoads], const uint8_t*& from, int32_t& left) {
+      const uint8_t* at = from;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int r = row + i * kConvWarps * kRows;
         w[i] = make_uint4(0, 0, 0, 0);
-        if (r < kTile && kt * kTile + r < kend) w[i] = load_global(reinterpret_cast<const uint4*>(base + (int64_t)(kt * kTile + r) * c.ld));
+        if (row + i * kStep < kTile && i * kStep < left) w[i] = load_global(reinterpret_cast<const uint4*>(at));
+        at += (int64_t)kStep * c.ld;
+      }
+      from += (int64_t)kTile * c.ld;
+      left -= kTile;
+    };
+    // A row's place in a tile: kStep rows on, the swizzle's row bits change by kStep & 7, which is 0 or 4.
+    static_assert(kStep % 4 == 0, "the swizzle of a lane's next row");
+    const uint32_t place = sKV + sw_offset(row, 2 * u);
+    auto widen = [&](const uint4 (&w)[kLoads], int slot) {
+      const uint32_t dst = place + slot * C::kTileBytes;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        if (row + i * kStep >= kTile) break;
+        const uint32_t to = (dst ^ ((i * kStep & 4) << 4)) + i * kStep * 128;
+        st_shared16(to, cvt_lo(w[i].x), cvt_hi(w[i].x), cvt_lo(w[i].y), cvt_hi(w[i].y));
+        st_shared16(to ^ 16, cvt_lo(w[i].z), cvt_hi(w[i].z), cvt_lo(w[i].w), cvt_hi(w[i].w));
       }
     };
-    auto widen = [&](const uint4 (&w)[kLoads], int slot) {
-      const uint32_t dst = sKV + slot * C::kTileBytes;
+    // the same times 2^shift, the lane's shift that of its group of keys
+    auto widen_shifted = [&](const uint4 (&w)[kLoads], int slot, int shift) {
+      const uint32_t dst = place + slot * C::kTileBytes;
+      const uint32_t by = pack_f16x2(exp2_int(shift), exp2_int(shift));
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int r = row + i * kConvWarps * kRows;
+        const int r = row + i * kStep;
+        const uint32_t f = __shfl_sync(0xffffffffu, by, NG == 1 ? 0 : min(r / kGroupKeys, NG - 1));
         if (r >= kTile) break;
-        st_shared16(dst + sw_offset(r, 2 * u), cvt_lo(w[i].x), cvt_hi(w[i].x), cvt_lo(w[i].y), cvt_hi(w[i].y));
-        st_shared16(dst + sw_offset(r, 2 * u + 1), cvt_lo(w[i].z), cvt_hi(w[i].z), cvt_lo(w[i].w), cvt_hi(w[i].w));
+        const uint32_t to = (dst ^ ((i * kStep & 4) << 4)) + i * kStep * 128;
+        st_shared16(to, mul_f16x2(cvt_lo(w[i].x), f), mul_f16x2(cvt_hi(w[i].x), f), mul_f16x2(cvt_lo(w[i].y), f),
+                    mul_f16x2(cvt_hi(w[i].y), f));
+        st_shared16(to ^ 16, mul_f16x2(cvt_lo(w[i].z), f), mul_f16x2(cvt_hi(w[i].z), f), mul_f16x2(cvt_lo(w[i].w), f),
+                    mul_f16x2(cvt_hi(w[i].w), f));
       }
     };
     auto empty = [&](int L) {
@@ -293,26 +357,62 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (lane == 0) mbar_arrive(bar_kv_full + 8 * (L % kSlots));
     };
     if (n_vis > 0) {
-      load(wk, kb, kt0);
-      load(wv, vb, kt0);
+      load(wk, kp, left_k);
+      load(wv, vp, left_v);
     }
-    for (int j = 0; j < n_vis; ++j) {
-      const int32_t kt = kt0 + j;
-      float4 sc = make_float4(1.f, 0.f, 0.f, 0.f);  // a group behind the end: finite, and every key masked
-      if (cw == 0 && lane < NG && kt * kTile + lane * kGroupKeys < kend) {
-        const int64_t at = (int64_t)bg * c.n_blocks + kt * NG + lane;
-        sc.x = load_global(c.k_scale + at);
-        scale_log2_parts(load_global(c.v_scale + at), sc.y, sc.z);
+    int32_t top = INT_MIN;
+    if (n_vis > 0 && warp_wait(bar_span, 0, p.status, kWhereKv8Widen)) top = *reinterpret_cast<volatile int32_t*>(vs_top);
+    if (top != INT_MIN) {
+      int unit = top;  // (every warp finds the same units and shifts: nothing is exchanged for them)
+#pragma unroll 1
+      for (int j = 0; j < n_vis; ++j) {
+        float4 sc = make_float4(1.f, 0.f, 0.f, 0.f);  // a group behind the end: finite, and every key masked
+        int shift = 0;
+        const int32_t g = (kt0 + j) * NG + lane;
+        const bool live = lane < NG && g * kGroupKeys < kend;
+        if (live) {
+          sc.x = load_global(c.k_scale + (int64_t)bg * c.n_blocks + g);
+          scale_log2_parts(load_global(c.v_scale + (int64_t)bg * c.n_blocks + g), sc.y, sc.z);
+        }
+        const int e = live ? (int)ceilf(sc.y) : INT_MIN;
+        const int hi = __reduce_max_sync(0xffffffffu, e), lo = __reduce_min_sync(0xffffffffu, live ? e : INT_MAX);
+        unit = max(hi - kShiftHi, min(unit, lo - kShiftLo));
+        sc.w = (float)unit;
+        if (live) {
+          const int by = max(e, unit + kShiftLo);
+          shift = by - unit;
+          sc.y -= (float)by;
+          sc.z *= exp2_int(min(max(by, -126), 127));
+        }
+        if (!empty(2 * j)) break;
+        widen(wk, (2 * j) % kSlots);
+        if (cw == 0 && lane < NG) scales[(j & 3) * NG + lane] = sc;
+        full(2 * j);
+        if (j + 1 < n_vis) load(wk, kp, left_k);
+        if (!empty(2 * j + 1)) break;
+        widen_shifted(wv, (2 * j + 1) % kSlots, shift);
+        full(2 * j + 1);
+        if (j + 1 < n_vis) load(wv, vp, left_v);
       }
-      if (!empty(2 * j)) break;
-      widen(wk, (2 * j) % kSlots);
-      if (cw == 0 && lane < NG) scales[(j & 3) * NG + lane] = sc;
-      full(2 * j);
-      if (j + 1 < n_vis) load(wk, kb, kt + 1);
-      if (!empty(2 * j + 1)) break;
-      widen(wv, (2 * j + 1) % kSlots);
-      full(2 * j + 1);
-      if (j + 1 < n_vis) load(wv, vb, kt + 1);
+    } else {
+      for (int j = 0; j < n_vis; ++j) {
+        const int32_t kt = kt0 + j;
+        float4 sc = make_float4(1.f, 0.f, 0.f, 0.f);  // a group behind the end: finite, and every key masked
+        if (cw == 0 && lane < NG && kt * kTile + lane * kGroupKeys < kend) {
+          const int64_t at = (int64_t)bg * c.n_blocks + kt * NG + lane;
+          sc.x = load_global(c.k_scale + at);
+          scale_log2_parts(load_global(c.v_scale + at), sc.y, sc.z);
+        }
+        if (!empty(2 * j)) break;
+        widen(wk, (2 * j) % kSlots);
+        if (cw == 0 && lane < NG) scales[(j & 3) * NG + lane] = sc;
+        full(2 * j);
+        if (j + 1 < n_vis) load(wk, kp, left_k);
+        if (!empty(2 * j + 1)) break;
+        widen(wv, (2 * j + 1) % kSlots);
+        full(2 * j + 1);
+        if (j + 1 < n_vis) load(wv, vp, left_v);
+      }
     }
     }
   } else {
@@ -378,7 +478,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t o_addr = tmem_base + ((uint32_t)lane_base << 16) + C::o_col(t);
     const int32_t lim = valid ? row_limit(p, r, len) : kend;  // padding rows see all: they never force the masks
     const bool live = __any_sync(0xffffffffu, valid);  // the warp has a row to answer for
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, unit = 0.f;  // O is in units of 2^unit
     bool ok = true;
     if (t == 0 || two) {
 #pragma unroll 1
@@ -430,6 +530,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if constexpr (NG <= 4) kept[g] = k;
           m_new = fmaxf(m_new, fmaf(x, fac * k.x, k.y));
         }
+        const float unit_now = sc[0].w;
+        const bool moved = unit_now != unit;  // (before the first product too, which does not read O)
         const bool first = m == -INFINITY;
         const bool need = !first && m_new > m + kFollow;
         float factor = 1.f;
@@ -440,7 +542,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           m = m_new;
           l *= factor;
         }
-        if (__any_sync(0xffffffffu, need)) {
+        if (__any_sync(0xffffffffu, need || moved)) {
+          if (moved) factor *= exp2_whole(fminf(fmaxf(unit - unit_now, -126.f), 126.f));
+          unit = unit_now;
 #pragma unroll 1
           for (int i = 0; i < HD / 32; ++i) {
             uint32_t ov[32];
@@ -503,7 +607,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const bool store = valid && dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store);
       const bool none = l == 0.f;  // the row saw nothing here
       const int64_t pr = (int64_t)slot_of_part * 2 * kTile + t * kTile + lane_base + lane;
-      const float inv = splits > 1 ? 1.f : 1.f / l;
+      const float inv = (splits > 1 ? 1.f : 1.f / l) * exp2_whole(unit);
       if (store && ok) {
         if (splits > 1)
           p.part_ml[pr] = make_float2(none ? -INFINITY : ref, l);

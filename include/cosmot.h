@@ -444,7 +444,12 @@ typedef struct {
  * [batch][n_heads][n_q], the natural logarithm of each softmax's sum.  A row
  * that sees nothing gives 0 and -infinity.  A query row with a NaN or an
  * infinity gives NaN; a NaN among a sequence's shown keys or values may reach
- * all of its queries.  workspace: cosmot_kv8_attention_workspace bytes
+ * all of its queries.  Weights are rounded to 11 bits, and to 2^-33 of the row's
+ * largest below 2^-22 of it.  Where a key head has more than 32 rows (queries x
+ * its heads) and an aligned run of 128 cached rows holds value scales more than
+ * 2^22 apart, weights of rows whose scale is 2^(22 + d) below the run's largest
+ * are rounded to 2^(d - 33) of the row's largest; otherwise scales may lie as far
+ * apart as they like within [2^-40, 2^40].  workspace: cosmot_kv8_attention_workspace bytes
  * (256-byte aligned, may be NULL when that is 0), for this call alone: calls
  * that may run at the same time need their own.
  */

@@ -120,21 +120,45 @@ def test_a_row_does_not_depend_on_the_rows_beside_it(n):
     check_attend(c, q, [1300], False)
 
 
-@pytest.mark.parametrize("n", [1, 3, 8])
-@pytest.mark.parametrize("large,small", [(20, -13), (40, -40), (3, -25), (-13, 20)])
+@pytest.mark.parametrize("n,block,large,small", [
+    *((n, 32, a, b) for n in (1, 3, 8) for a, b in ((20, -13), (40, -40), (3, -25), (-13, 20))),
+    *((n, 128, a, b) for n in (1, 40, 150, 300) for a, b in ((20, -13), (40, -40), (3, -25), (-13, 20))),
+    *((n, block, a, b) for n in (40, 150, 300) for block in (16, 32, 64) for a, b in ((10, -10), (-30, -38), (40, 20), (-12, 8)))])
 @pytest.mark.parametrize("causal", [False, True])
-def test_a_large_scale_over_small_bytes_hides_no_other_value(n, large, small, causal):
+def test_a_large_scale_over_small_bytes_hides_no_other_value(n, block, large, small, causal):
     """The bound is relative to the values, not to their blocks' scales: a block of a large scale whose rows are zero
-    (an outlier row that went, or that the mask hides) leaves the others' digits alone."""
-    lens = [400, 133]
-    c = filled(2, 400, 2, 128, 32, lens, seed=230)
-    c.v_scale[:, :, :12] = 2.0 ** small * torch.tensor([1.0, 2.0, 4.0] * 4, device="cuda")
-    c.v_scale[:, 0, 1::4] = 2.0 ** large
-    c.v_scale[:, 1, 0:12:3] = 2.0 ** large
+    (an outlier row that went, or that the mask hides) leaves the others' digits alone.  More than 32 packed rows: the
+    blocks of an aligned run of 128 rows have scales within 2^22."""
+    lens = [1300, 530]
+    nb = -(-1300 // block)
+    c = filled(2, 1300, 2, 128, block, lens, seed=230)
+    c.v_scale[:] = 2.0 ** small * torch.tensor([1.0, 2.0, 4.0], device="cuda").repeat(nb)[:nb]
     for h, first, step in ((0, 1, 4), (1, 0, 3)):
-        for j in range(first, 12, step):
-            c.v.view(torch.uint8)[:, 32 * j:32 * j + 32, h] = 0
+        c.v_scale[:, h, first::step] = 2.0 ** large
+        for j in range(first, nb, step):
+            c.v.view(torch.uint8)[:, block * j:block * (j + 1), h] = 0
     for b, m in enumerate(lens):  # nothing reads the scales of blocks without a row
-        c.v_scale[b, :, -(-m // 32):] = math.nan
+        c.v_scale[b, :, -(-m // block):] = math.nan
     q = queries(231, 2, n, 4, 128)
     check_attend(c, q, lens, causal)
+
+
+@pytest.mark.parametrize("n", [40, 300])
+@pytest.mark.parametrize("large,small", [(20, -13), (22, -14)])
+def test_scales_too_far_apart_in_one_run_lose_the_digits_that_are_stated(n, large, small):
+    """Blocks of 32 in runs of 128 rows, scales 2^(22 + d) apart: weights are right to 2^(d - 33) of the largest."""
+    lens, block, d = [1300], 32, large - small - 22
+    c = filled(1, 1300, 1, 128, block, lens, seed=232)
+    c.v_scale[:] = 2.0 ** small
+    c.v_scale[:, :, 1::4] = 2.0 ** large
+    for j in range(1, c.n_blocks, 4):
+        c.v.view(torch.uint8)[:, block * j:block * (j + 1)] = 0
+    q = queries(233, 1, n, 2, 128)
+    o, lse = c.attend(q)
+    K, V = dequant(c, lens)
+    ro, rl, bo, bl, _ = P.attend(q, K, V, lens, False)
+    for h in range(2):
+        w = torch.exp(q[0, :, h].double() @ K[0, :, 0].T / math.sqrt(128) - rl[0, h][:, None])
+        bo[0, :, h] += 2.0 ** (d - 33) * w.amax(1, keepdim=True) * V[0, :, 0].abs().sum(0)
+    assert bool(((o.double() - ro).abs() <= bo).all()) and bool(((lse.double() - rl).abs() <= bl).all())
+    assert_device_ok()
