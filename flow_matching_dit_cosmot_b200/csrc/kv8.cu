@@ -283,6 +283,7 @@ __global__ void __launch_bounds__(kSelectThreads)
   }
   __syncthreads();
   for (int32_t j = count + tid; j < c.n_blocks; j += kSelectThreads) {
+    if (!dcheck(j >= 0 && count <= nb && nb <= c.n_blocks, status, kWhereKv8Store)) break;
     if (j < nb)
       weight_out[base + j] = 0.f;  // blocks that a later store begins anew
     else if (weight_out != weight)
@@ -304,7 +305,8 @@ constexpr int kMoveThreads = 128, kMoveTurn = 8, kMoveRing = 24;
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ Cache c,
                                                                   const EvictPlan* plan,
-                                                                  const int32_t* list, int32_t* lens_out) {
+                                                                  const int32_t* list, int32_t* lens_out,
+                                                                  int* status) {
   pdl_trigger();
   pdl_wait();
   const int32_t b = blockIdx.y / c.n_kv, g = blockIdx.y % c.n_kv;
@@ -327,7 +329,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   int32_t next[kMoveTurn];
   auto look = [&](int32_t j) {
 #pragma unroll
-    for (int i = 0; i < kMoveTurn; ++i) next[i] = j + i < end ? src[j + i] : 0;
+    for (int i = 0; i < kMoveTurn; ++i) {
+      next[i] = j + i < end ? src[j + i] : 0;
+      // a source behind its destination, both inside the cache; else (debug build) the block stays as it is
+      if (j + i < end && !dcheck(next[i] >= j + i && (int64_t)next[i] * c.block + r < c.capacity, status, kWhereKv8Store))
+        next[i] = j + i;
+    }
   };
   auto read = [&](int32_t j, int slot) {  // kMoveTurn blocks from j on, whose sources `next` holds
 #pragma unroll
@@ -358,7 +365,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
                    : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
                    : "r"(at + (slot * kMoveTurn + i) * (kMoveThreads * 16))
                    : "memory");
-      if (j + i < end) *reinterpret_cast<uint4*>(base + (j + i) * step) = x;
+      if (j + i < end && dcheck((int64_t)(j + i) * c.block + r < c.capacity, status, kWhereKv8Store))
+        *reinterpret_cast<uint4*>(base + (j + i) * step) = x;
     }
     slot = slot == kTurns - 1 ? 0 : slot + 1;
   }
@@ -519,6 +527,7 @@ extern "C" cosmot_status cosmot_kv8_attention(const cosmot_kv8_cache* cache, con
   if (!tiles && need > 0) {
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kv8::o_part_bytes(c, p));
+    p.part_rows = (int64_t)p.splits * c.batch * c.n_kv * p.n_rows;
   }
   if (p.n_q == 0) return COSMOT_OK;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -585,5 +594,5 @@ extern "C" cosmot_status cosmot_kv8_evict(const cosmot_kv8_cache* cache, const f
   const unsigned slices = (unsigned)((c.block * c.hd / 16 + kv8::kMoveThreads - 1) / kv8::kMoveThreads);  // 64 .. 1024 pieces
   return launch_status(launch_pdl(kv8::evict_move_kernel, dim3(slices, (unsigned)(c.batch * c.n_kv), 2),
                                   dim3(kv8::kMoveThreads), 0, s, nullptr, c, (const kv8::EvictPlan*)plan,
-                                  (const int32_t*)list, lens_out));
+                                  (const int32_t*)list, lens_out, status));
 }

@@ -51,6 +51,7 @@ struct Query {
   int32_t splits, chunk;  // chunk: keys of a split (register-tile kernels)
   float* part_o;
   float2* part_ml;
+  int64_t part_rows;  // rows that the workspace has room for (debug store checks)
   int* status;
 };
 

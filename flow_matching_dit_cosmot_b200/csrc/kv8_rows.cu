@@ -202,8 +202,9 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
   const int32_t k0 = (int32_t)min((int64_t)shown, (int64_t)split * p.chunk);
   const int32_t kend = split == p.splits - 1 ? shown : (int32_t)min((int64_t)shown, (int64_t)(split + 1) * p.chunk);
   if (p.splits > 1 && k0 >= kend) {  // nothing here: the join leaves this range out
-    if (r0 + threadIdx.x < r_end && threadIdx.x < 8 * NT)
-      p.part_ml[((int64_t)split * c.batch * c.n_kv + blockIdx.z) * p.n_rows + r0 + threadIdx.x] = make_float2(-INFINITY, 0.f);
+    const int64_t pr = ((int64_t)split * c.batch * c.n_kv + blockIdx.z) * p.n_rows + r0 + threadIdx.x;
+    if (r0 + threadIdx.x < r_end && threadIdx.x < 8 * NT && dcheck(pr < p.part_rows, p.status, kWhereKv8Store))
+      p.part_ml[pr] = make_float2(-INFINITY, 0.f);
     return;
   }
 
@@ -425,6 +426,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
     ref -= kPBias;
     if (p.splits > 1) {
       const int64_t pr = ((int64_t)split * c.batch * c.n_kv + blockIdx.z) * p.n_rows + r;
+      if (!dcheck(pr < p.part_rows, p.status, kWhereKv8Store)) continue;
       *reinterpret_cast<float4*>(p.part_o + pr * HD + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
       if (col == 0) p.part_ml[pr] = make_float2(lsum == 0.f ? -INFINITY : ref, lsum);
     } else {

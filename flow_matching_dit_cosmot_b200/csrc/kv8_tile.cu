@@ -604,9 +604,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ok = ok && warp_wait(bar_o_done, 0, p.status, kWhereKv8Softmax);
         tc_fence_after();
       }
-      const bool store = valid && dcheck(qi < p.n_q && h < p.n_heads, p.status, kWhereKv8Store);
       const bool none = l == 0.f;  // the row saw nothing here
       const int64_t pr = (int64_t)slot_of_part * 2 * kTile + t * kTile + lane_base + lane;
+      const bool store = valid && dcheck(qi < p.n_q && h < p.n_heads && (splits == 1 || (pr >= 0 && pr < p.part_rows)),
+                                         p.status, kWhereKv8Store);
       const float inv = (splits > 1 ? 1.f : 1.f / l) * exp2_whole(unit);
       if (store && ok) {
         if (splits > 1)
@@ -1285,6 +1286,7 @@ cosmot_status tile_attention(const Cache& c, const Query& p0, int32_t max_len, v
   if (t.n_parts()) {
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan_o_bytes(t, c.hd));
+    p.part_rows = (int64_t)t.n_parts() * 2 * kTile;
   }
   return c.hd == 128 ? launch_attention<128>(c, p, t, s) : launch_attention<64>(c, p, t, s);
 }

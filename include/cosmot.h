@@ -86,7 +86,7 @@ COSMOT_API cosmot_status cosmot_get_device_status(cosmot_stream_t stream, cosmot
  * 1 in the debug build of the library (libcosmot_debug.so, compiled with
  * COSMOT_DEBUG_CHECKS), 0 in the release build.  The debug build checks the
  * index of every global store its kernels make (GEMM, attention, norm and
- * Euler outputs) against the extent the host side derived for that output; a
+ * Euler outputs; the 8-bit cache's rows, moves and partial results) against the extent the host side derived for that output; a
  * failed check latches COSMOT_ERR_BOUNDS with the kernel's site code into the
  * device status word and skips the store (no trap).  Results are otherwise
  * identical to the release build's.

@@ -162,3 +162,28 @@ def test_scales_too_far_apart_in_one_run_lose_the_digits_that_are_stated(n, larg
         bo[0, :, h] += 2.0 ** (d - 33) * w.amax(1, keepdim=True) * V[0, :, 0].abs().sum(0)
     assert bool(((o.double() - ro).abs() <= bo).all()) and bool(((lse.double() - rl).abs() <= bl).all())
     assert_device_ok()
+
+
+# ------------------------------------------------------------------ the debug build
+
+@pytest.mark.parametrize("lens,n,g,group,block,keep", [([5000], 1, 2, 4, 16, 40), ([3000, 700], 40, 2, 1, 64, 7),
+                                                       ([2600, 0, 90], 200, 1, 2, 128, 5), ([12_000], 3, 1, 8, 32, 600)])
+def test_the_debug_build_agrees_on_split_keys_and_moves(lens, n, g, group, block, keep):
+    """Its checks of the partial results' places and of the moves' sources and destinations find nothing."""
+    outs = []
+    release = L.lib()
+    for lib in (release, L.lib_debug()):
+        L._lib = lib
+        try:
+            c = scattered(len(lens), max(lens), g, 64, block, lens, seed=250)
+            q = queries(251, len(lens), n, g * group, 64) * 0.2
+            o, lse = c.attend(q)
+            w = c.weigh(q, lse, c.empty_weight())
+            c.evict(w, keep, 20, 30)
+            torch.cuda.synchronize()
+            assert_device_ok()
+        finally:
+            L._lib = release
+        outs.append((o, lse, w, c.lens, c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_scale, c.v_scale))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)

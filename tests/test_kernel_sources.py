@@ -60,3 +60,19 @@ def test_no_load_of_an_earlier_kernels_output_may_pass_the_wait_for_it(name):
                 assert var in CONSTANTS, f"{m.group(1)}: {var} is read"
             else:
                 assert WRITTEN_ONLY.get(m.group(1)) == var, f"{m.group(1)}: {var} may be read"
+
+
+# Places that write global memory in the 8-bit cache's kernels, and how many of them the debug build checks: every one
+# whose index is not the thread's own loop variable below its extent.
+KV8_CHECKS = {"store_kernel": 2, "evict_select_kernel": 2, "evict_move_kernel": 2, "tile_attention_kernel": 1, "tile_join_kernel": 1,
+              "tile_weigh_kernel": 1, "rows_attention_kernel": 3, "rows_join_kernel": 1, "rows_weigh_kernel": 1}
+
+
+def test_the_debug_build_checks_every_store_of_the_8_bit_cache():
+    seen = {}
+    for name in [f for f in FILES if f.startswith("kv8")]:
+        text = re.sub(r"__launch_bounds__\((?:[^()]|\([^()]*\))*\)", "", source(name))
+        parts = re.split(r"__global__[^;{(]*?(\w+)\(", text)
+        for kernel, body in zip(parts[1::2], parts[2::2]):
+            seen[kernel] = body.split("\n}\n")[0].count("dcheck(")
+    assert seen == KV8_CHECKS
