@@ -298,11 +298,11 @@ class KVCache8:
         cache.advance(n)                               # after the last denoising step
         cache.evict(weight, keep_blocks, first_rows=n_ar, last_rows=n)
 
-    Every call runs on `stream` (default: the current one of the cache's device)
-    and follows `lens` on the device, so it may be captured into a CUDA graph.
-    Outputs and workspaces that a call makes are its own; on another stream it
-    first waits for the current one, whose memory they are.  A workspace given by
-    the caller serves one call at a time.
+    Every call, advance too, runs on `stream` (default: the current one of the
+    cache's device) and follows `lens` on the device, so it may be captured into a
+    CUDA graph.  On another stream a call first waits for what the current one has
+    been given so far.  Outputs and workspaces that a call makes are its own.  A
+    workspace given by the caller serves one call at a time.
     The library reports lengths outside the cache through the device status.
     """
 
@@ -355,18 +355,18 @@ class KVCache8:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
 
     def _stream(self, stream, *made) -> int:
-        """The stream's handle.  Tensors made here come from the current stream's memory: another
-        stream waits for what that stream still does with it, and they are kept until it is done."""
+        """The stream's handle.  Another stream than the current one first waits for that one, which
+        may still write the inputs and owns the memory of tensors made here; they are kept until the
+        other is done."""
         if stream is None:  # torch.cuda.current_stream(device).cuda_stream, without the object
             return torch._C._cuda_getCurrentRawStream(self.device.index)
         if stream.device != self.device:
             raise ValueError(f"the stream is on {stream.device}, the cache on {self.device}")
-        made = [t for t in made if t is not None]
-        if made:
-            current = torch.cuda.current_stream(self.device)
-            if current != stream:
-                stream.wait_stream(current)
-                for t in made:
+        current = torch.cuda.current_stream(self.device)
+        if current != stream:
+            stream.wait_stream(current)
+            for t in made:
+                if t is not None:
                     t.record_stream(stream)
         return stream.cuda_stream
 
@@ -417,9 +417,14 @@ class KVCache8:
         self._here("q", q)
         return plan
 
-    def advance(self, n: int):
-        """The last n stored rows become rows held (on the current stream)."""
-        self.lens.add_(n)
+    def advance(self, n: int, stream=None):
+        """The last n stored rows become rows held."""
+        if stream is None:
+            self.lens.add_(n)
+            return
+        self._stream(stream)
+        with torch.cuda.stream(stream):
+            self.lens.add_(n)
 
     def store(self, k: torch.Tensor, v: torch.Tensor, stream=None):
         """Rows [batch, n, n_kv_heads, head_dim] (bf16, views of a QKV projection
@@ -487,7 +492,9 @@ class KVCache8:
         the ones that hold the first first_rows or the last last_rows rows, or a
         part of a block, then those of the most weight.  The cache's rows and
         scales move up in place; (weight, lens) follow in place too, or, with
-        in_place=False, are returned as new tensors."""
+        in_place=False, are returned as new tensors: the cache then still goes by
+        the old lengths, and is not to be used before the new ones are copied into
+        `lens`."""
         self._check("weight", weight, torch.float32, (self.batch, self.n_kv_heads, self.n_blocks))
         self._here("weight", weight)
         w_out, lens = (weight, self.lens) if in_place else (torch.empty_like(weight), torch.empty_like(self.lens))

@@ -187,3 +187,66 @@ def test_the_debug_build_agrees_on_split_keys_and_moves(lens, n, g, group, block
         outs.append((o, lse, w, c.lens, c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_scale, c.v_scale))
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ streams
+
+def _late(t, seconds=0.02):
+    """A copy of t that the current stream makes only after some work."""
+    out = torch.zeros_like(t)
+    torch.cuda._sleep(int(seconds * 1.5e9))
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("n", [1, 150])
+def test_a_streaming_step_on_another_stream_is_the_same(n):
+    """The documented step with stream= on every call, its inputs still being made on the current stream."""
+    make = lambda: scattered(2, 900, 2, 64, 16, [300, 41], seed=260)  # noqa: E731
+    a, b = make(), make()
+    wa, wb = a.empty_weight(), b.empty_weight()
+    s = torch.cuda.Stream()
+    for t in range(3):
+        x = rows(261 + t, 2, n, 8, 64) * 0.2
+        a.store(x[:, :, 4:6], x[:, :, 6:])
+        oa, la = a.attend(x[:, :, :4], n_new=n)
+        a.weigh(x[:, :, :4], la, wa, n_new=n)
+        a.advance(n)
+        a.evict(wa, 12, first_rows=10, last_rows=n)
+        torch.cuda.synchronize()
+        y = _late(x)
+        b.store(y[:, :, 4:6], y[:, :, 6:], stream=s)
+        ob, lb = b.attend(y[:, :, :4], n_new=n, stream=s)
+        b.weigh(y[:, :, :4], lb, wb, n_new=n, stream=s)
+        b.advance(n, stream=s)
+        b.evict(wb, 12, first_rows=10, last_rows=n, stream=s)
+        torch.cuda.synchronize()
+        for p, q in ((oa, ob), (la, lb), (wa, wb), (a.lens, b.lens), (a.k.view(torch.uint8), b.k.view(torch.uint8)),
+                     (a.v_scale, b.v_scale)):
+            assert torch.equal(p, q)
+    assert_device_ok()
+
+
+def test_store_on_another_stream_waits_for_its_inputs():
+    a, b = (scattered(1, 200, 2, 64, 16, [30], seed=265) for _ in range(2))
+    x = rows(266, 1, 100, 4, 64)
+    a.store(x[:, :, :2], x[:, :, 2:])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    y = _late(x)
+    b.store(y[:, :, :2], y[:, :, 2:], stream=s)
+    b.advance(100, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(a.k.view(torch.uint8), b.k.view(torch.uint8)) and b.lens.tolist() == [130]
+
+
+def test_weigh_on_another_stream_waits_for_its_inputs():
+    c = scattered(1, 900, 2, 64, 16, [900], seed=267)
+    q = queries(268, 1, 3, 4, 64) * 0.2
+    _, lse = c.attend(q)
+    want = c.weigh(q, lse, c.empty_weight())
+    torch.cuda.synchronize()
+    w = _late(c.empty_weight() + 1) - 1
+    c.weigh(q, lse, w, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert torch.equal(w, want)
