@@ -304,7 +304,17 @@ class KVCache8:
     been given so far.  Outputs and workspaces that a call makes are its own.  A
     workspace given by the caller serves one call at a time.
     The library reports lengths outside the cache through the device status.
+    The tensors stay the ones that the cache was made with (its kernels and captured
+    graphs go by their addresses): write into them, `lens.copy_(...)`.
     """
+
+    _FIXED = frozenset(("k", "v", "k_scale", "v_scale", "lens", "block", "batch", "capacity", "n_kv_heads", "head_dim", "n_blocks",
+                        "device"))
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED and hasattr(self, "desc") and value is not getattr(self, name):  # (lens += n is in place)
+            raise AttributeError(f"KVCache8.{name} is what the cache was made with; write into its tensors instead of replacing them")
+        super().__setattr__(name, value)
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
                  lens: torch.Tensor, block: int):

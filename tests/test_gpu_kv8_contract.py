@@ -250,3 +250,25 @@ def test_weigh_on_another_stream_waits_for_its_inputs():
     c.weigh(q, lse, w, stream=torch.cuda.Stream())
     torch.cuda.synchronize()
     assert torch.equal(w, want)
+
+
+# ------------------------------------------------------------------ the cache object
+
+def test_replacing_a_tensor_is_refused_and_copying_the_new_lengths_works():
+    """Out-of-place eviction returns new lengths; assigned, they would be without effect."""
+    a, b = (scattered(1, 300, 2, 64, 16, [300], seed=270) for _ in range(2))
+    w = torch.rand((1, 2, a.n_blocks), generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    wa, lens = a.evict(w, 7, in_place=False)
+    with pytest.raises(AttributeError):
+        a.lens = lens
+    for name in ("k", "v", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError):
+            setattr(a, name, getattr(b, name))
+    a.lens.copy_(lens)
+    a.lens += 1
+    a.lens -= 1
+    wb = w.clone()
+    b.evict(wb, 7)
+    q = queries(271, 1, 40, 4, 64) * 0.2
+    assert torch.equal(a.lens, b.lens) and torch.equal(wa, wb)
+    assert torch.equal(a.attend(q)[0], b.attend(q)[0])
