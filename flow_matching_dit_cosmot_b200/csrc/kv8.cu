@@ -415,8 +415,8 @@ cosmot_status make_query(const cosmot_kv8_cache* c, const cosmot_kv8_query* d, Q
   o = Query{};
   o.n_q = d->n_q;
   o.group = d->n_heads / c->n_kv_heads;
-  o.n_rows = d->n_q * o.group;
   if (d->n_q > INT32_MAX / 2 / o.group) return COSMOT_ERR_UNSUPPORTED;
+  o.n_rows = d->n_q * o.group;
   o.n_heads = d->n_heads;
   o.n_new = d->n_new;
   o.causal = d->mask_mode == COSMOT_KV8_CAUSAL;
@@ -498,6 +498,7 @@ extern "C" cosmot_status cosmot_kv8_attention_workspace(const cosmot_kv8_cache* 
   if (st == COSMOT_OK) st = kv8::make_query(cache, query, p);
   if (st != COSMOT_OK) return st;
   if (kv8::use_tiles(p)) {
+    if (!kv8::tile_fits(c, p)) return COSMOT_ERR_UNSUPPORTED;
     *bytes = kv8::tile_workspace(c, p, kv8::bound_len(cache, query));
     return COSMOT_OK;
   }
@@ -518,6 +519,7 @@ extern "C" cosmot_status cosmot_kv8_attention(const cosmot_kv8_cache* cache, con
   if (!o || !aligned16(o) || ld_o % 8 || ld_o < (int64_t)p.n_heads * c.hd) return COSMOT_ERR_INVALID_ARG;
   const int32_t max_len = kv8::bound_len(cache, query);
   const bool tiles = kv8::use_tiles(p);
+  if (tiles && !kv8::tile_fits(c, p)) return COSMOT_ERR_UNSUPPORTED;
   if (!tiles) kv8::rows_plan(c, p, max_len);
   const size_t need = tiles ? kv8::tile_workspace(c, p, max_len) : kv8::part_bytes(c, p);
   if (need > 0) {

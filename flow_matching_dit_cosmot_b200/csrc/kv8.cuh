@@ -144,6 +144,7 @@ cosmot_status rows_weigh(const Cache& c, const Query& p, float decay, float* wei
 void rows_plan(const Cache& c, Query& p, int32_t max_len);
 // tcgen05 kernels (kv8_tile.cu): many packed rows.  max_len: what the host
 // takes the longest sequence to show; it sizes the split of the work only.
+bool tile_fits(const Cache& c, const Query& p);  // else UNSUPPORTED: more work items than a grid counts
 size_t tile_workspace(const Cache& c, const Query& p, int32_t max_len);
 cosmot_status tile_attention(const Cache& c, const Query& p, int32_t max_len, void* workspace, cudaStream_t s);
 cosmot_status tile_weigh(const Cache& c, const Query& p, float decay, float* weight, int32_t max_len, cudaStream_t s);

@@ -1274,6 +1274,10 @@ cosmot_status launch_weigh(const Cache& c, const Query& p, float decay, float* w
 
 }  // namespace
 
+bool tile_fits(const Cache& c, const Query& p) {
+  return (int64_t)c.batch * c.n_kv * ((p.n_rows + 2 * kTile - 1) / (2 * kTile)) <= INT32_MAX / 64;
+}
+
 size_t tile_workspace(const Cache& c, const Query& p, int32_t max_len) {
   const TilePlan t = make_plan(c, p, max_len);
   return t.n_parts() == 0 ? 0 : plan_o_bytes(t, c.hd) + (size_t)t.n_parts() * 2 * kTile * sizeof(float2);
@@ -1282,7 +1286,6 @@ size_t tile_workspace(const Cache& c, const Query& p, int32_t max_len) {
 cosmot_status tile_attention(const Cache& c, const Query& p0, int32_t max_len, void* workspace, cudaStream_t s) {
   Query p = p0;
   const TilePlan t = make_plan(c, p, max_len);
-  if ((int64_t)c.batch * c.n_kv * t.pairs > INT32_MAX / 64) return COSMOT_ERR_UNSUPPORTED;
   if (t.n_parts()) {
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan_o_bytes(t, c.hd));
