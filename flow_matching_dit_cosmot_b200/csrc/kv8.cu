@@ -453,6 +453,11 @@ size_t part_bytes(const Cache& c, const Query& p) {
 constexpr int64_t kRowsMax = 32;
 bool use_tiles(const Query& p) { return p.n_rows > kRowsMax; }
 
+// A range of 256 keys is weighed by all the rows in one go, 1.5 us for 128 of
+// them, and the warps that wait for its end do so for a second at most: 2^25 rows
+// take 0.4 s.
+constexpr int64_t kWeighRowsMax = int64_t(1) << 25;
+
 size_t evict_list_offset(const Cache& c) { return ((size_t)c.batch * c.n_kv * sizeof(EvictPlan) + 255) & ~size_t(255); }
 
 }  // namespace
@@ -553,6 +558,7 @@ extern "C" cosmot_status cosmot_kv8_weigh(const cosmot_kv8_cache* cache, const c
   if (st == COSMOT_OK) st = kv8::check_q(cache, query, q, ld_q);
   if (st != COSMOT_OK) return st;
   if (!lse || !weight || !(decay >= 0.f) || decay > 1e30f) return COSMOT_ERR_INVALID_ARG;
+  if (p.n_rows > kv8::kWeighRowsMax) return COSMOT_ERR_UNSUPPORTED;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.ld_q = ld_q;
   p.lse = const_cast<float*>(lse);

@@ -25,3 +25,11 @@ def test_the_largest_calls_that_fit_have_a_workspace_of_a_wave_at_most(n_kv, n_q
     c = cache(batch=1, n_kv_heads=n_kv, ld=n_kv * 128, capacity=1_000_000)
     need = L.cosmot_kv8_attention_workspace(c, query(n_q=n_q, q_batch_stride=n_q, o_batch_stride=n_q, n_heads=n_kv))
     assert 0 <= need <= 6 * 160 * 256 * (128 * 4 + 8) + 256
+
+
+@pytest.mark.parametrize("n_q,group,want", [(2 ** 25 + 1, 1, L.COSMOT_ERR_UNSUPPORTED), (2 ** 22 + 1, 8, L.COSMOT_ERR_UNSUPPORTED),
+                                            (2 ** 30 - 1, 1, L.COSMOT_ERR_UNSUPPORTED)])
+def test_weighing_more_rows_than_its_waits_allow_is_refused(n_q, group, want):
+    c = cache(batch=1)
+    q = query(n_q=n_q, q_batch_stride=n_q, o_batch_stride=n_q, n_heads=2 * group)
+    assert L.lib().cosmot_kv8_weigh(ctypes.byref(c), ctypes.byref(q), 256, 2 * group * 128, 256, 1.0, 256, None) == want
