@@ -374,9 +374,8 @@ COSMOT_API cosmot_status cosmot_flow_cfg_euler_step(void* x_cond, void* x_base, 
  * bf16 cache, so rows may be dropped without touching the others.
  *   k, v     device e4m3 [batch][batch_stride rows][ld], heads of head_dim from
  *            element 0; 16-byte aligned, ld a multiple of 16
- *   k_scale, v_scale  device float32 [batch][n_kv_heads][ceil(capacity / block)];
- *            positive, and those of values within [2^-40, 2^40] (what
- *            cosmot_kv8_store writes)
+ *   k_scale, v_scale  device float32 [batch][n_kv_heads][ceil(capacity / block)],
+ *            within [2^-40, 2^40] (what cosmot_kv8_store writes)
  *   lens     device int32 [batch]: rows that each sequence holds, [0, capacity].
  *            The kernels read it, so a captured graph follows it.  A value
  *            outside (or without room for the rows of the call) is reported as
@@ -443,15 +442,16 @@ typedef struct {
  * 16-byte aligned with ld % 8 == 0.  lse: NULL, or device float32
  * [batch][n_heads][n_q], the natural logarithm of each softmax's sum.  A row
  * that sees nothing gives 0 and -infinity.  A query row with a NaN or an
- * infinity gives NaN; a NaN among a sequence's shown keys or values may reach
- * all of its queries.  Weights are rounded to 11 bits, and to 2^-33 of the row's
- * largest below 2^-22 of it.  Where a key head has more than 32 rows (queries x
- * its heads) and an aligned run of 128 cached rows holds value scales more than
- * 2^22 apart, weights of rows whose scale is 2^(22 + d) below the run's largest
- * are rounded to 2^(d - 33) of the row's largest; otherwise scales may lie as far
- * apart as they like within [2^-40, 2^40].  workspace: cosmot_kv8_attention_workspace bytes
- * (256-byte aligned, may be NULL when that is 0), for this call alone: calls
- * that may run at the same time need their own.
+ * infinity, or with scores beyond float32, gives NaN; a NaN among a sequence's
+ * shown keys or values may reach all of its queries.  Weights are rounded to 11
+ * bits, and to 2^-33 of the row's largest below 2^-22 of it.  Value scales may
+ * lie as far apart as they like, but for this: where a key head has more than 32
+ * rows (queries x its heads) and the blocks of an aligned run of 128 cached rows
+ * have scales more than 2^22 apart, weights of rows whose scale is 2^(22 + d)
+ * below the run's largest are rounded to 2^(d - 33) of the row's largest.
+ * workspace: cosmot_kv8_attention_workspace bytes (256-byte aligned, may be NULL
+ * when that is 0), for this call alone: calls that may run at the same time need
+ * their own.
  */
 COSMOT_API cosmot_status cosmot_kv8_attention_workspace(const cosmot_kv8_cache* cache, const cosmot_kv8_query* query,
                                                         size_t* bytes);
@@ -466,7 +466,8 @@ COSMOT_API cosmot_status cosmot_kv8_attention(const cosmot_kv8_cache* cache, con
  * for the blocks that hold a shown row; the others are left as they are.
  * weight: device float32 [batch][n_kv_heads][ceil(capacity / block)]; lse as
  * cosmot_kv8_attention wrote it for the same query (rows of -infinity add
- * nothing).  decay >= 0.
+ * nothing).  decay >= 0.  UNSUPPORTED above 2^25 rows (queries x heads of a key
+ * head); call it for parts of a FULL query then, the later ones with decay 1.
  */
 COSMOT_API cosmot_status cosmot_kv8_weigh(const cosmot_kv8_cache* cache, const cosmot_kv8_query* query, const void* q,
                                           int64_t ld_q, const float* lse, float decay, float* weight,
