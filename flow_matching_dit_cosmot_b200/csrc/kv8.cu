@@ -13,11 +13,11 @@ namespace kv8 {
 // elements, still in registers, are rounded against the scale, so every input
 // byte is read once.  Rows of the block that were there before are read only if
 // the scale grows.
-// bound: HBM (4 bytes read and 2 written for each K and V element).  18,978 rows
-// x 32 heads of 128: 88 us = 5.3 TB/s.  256 threads at four CTAs an SM took 82
-// us where 512 took 99 and 128 the same; magnitudes on packed bits saved 12 us
-// (the float form kept the issue slots 72 % busy).  1,560 rows: 10.8 us at six
-// CTAs an SM, 11.9 at four.
+// bound: HBM (4 bytes read and 2 written for each K and V element), the issue
+// slots next (78 % busy).  18,978 rows x 32 heads of 128: 82 to 89 us = 5.7 to
+// 5.3 TB/s.  256 threads at four CTAs an SM; 512 took 99 us where they took 82,
+// 128 the same; magnitudes on packed bits saved 12 us.  1,560 rows: 9.8 to 10.8
+// us at six CTAs an SM, 11.9 at four.
 constexpr int kStoreThreads = 256;
 
 // Largest of the CTA's values: magnitudes of bf16 order like their bits.
@@ -129,8 +129,8 @@ __global__ void __launch_bounds__(kStoreThreads, kUnits <= 4 ? 6 : 4)
 // the ordered bits of the weights (four passes of 8 bits) gives the threshold.
 // Then one pass in index order lists the blocks that stay and moves their scales
 // and weights.  The second kernel moves the rows.
-// 1,560 of 14,106 rows x 32 heads go: 49 us, the moves 41 of them (198 MB, read
-// and write in turn) against 30 at the copy's rate.
+// 1,560 of 14,106 rows x 32 heads go: 47 to 49 us, the moves 41 of them (198 MB,
+// read and write in turn) against 30 at the copy's rate.
 constexpr int kSelectThreads = 512;
 
 struct EvictPlan {  // per sequence and head, in the workspace
@@ -448,8 +448,10 @@ size_t part_bytes(const Cache& c, const Query& p) {
 
 // Up to kRowsMax packed rows the register-tile kernels run, above it the tcgen05
 // ones.  Attention, 14,106 rows x 32 heads: 53 against 61 us at 32 rows, 71
-// against 63 at 48; x 8 heads: 23 against 30, at 64 31 against 32.  Weighing, 32
-// heads: 44 against 57 at 32, 63 against 57 at 48.
+// against 63 at 48.  Weighing, 32 heads: 44 against 57 at 32, 63 against 57 at 48.
+// The rule looks at the rows alone: x 8 heads the register tiles take 23 us where
+// the others take 30 at 32 rows and still 31 against 32 at 64, so that 33 to 63
+// rows on few heads would go a little faster there.
 constexpr int64_t kRowsMax = 32;
 bool use_tiles(const Query& p) { return p.n_rows > kRowsMax; }
 

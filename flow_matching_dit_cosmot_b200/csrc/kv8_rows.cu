@@ -180,7 +180,7 @@ struct Ring {
 
 // One CTA per (key range, 8 NT packed rows, sequence and key head); its warps
 // take 16 keys in turn.
-// bound: HBM.  One token behind 130,999 rows (8 key heads of 128): 57 us with
+// bound: HBM.  One token behind 130,999 rows (8 key heads of 128): 57.5 us with
 // the join, the ranges alone 51 us = 5.2 TB/s; without the arithmetic the same
 // loads take 46.  Three stages at four CTAs an SM, four at three and six at two
 // are within 2 % of one another.

@@ -44,9 +44,10 @@
 // per group of 16 keys it adds 2^(s f - lse).  Nothing but the sums leaves the
 // CTA; a cluster may share the queries of one key range, and the sums are
 // joined in a fixed order.  A quarter of the exponentials runs on the FMA pipe.
-// bound: the SFU (62 % busy) and the issue slots (64 %).  The same sizes: 213 us
-// (an SFU floor of 156; the products alone 131); with every exponential on the
-// SFU 257 where a quarter off it took 233, three eighths 244.
+// bound: the SFU (62 % busy) and the issue slots (64 %).  The same sizes: 230 us
+// in long runs, 213 on a cool card (an SFU floor of 156; the products alone 131);
+// with every exponential on the SFU 257 where a quarter off it took 233, three
+// eighths 244.
 #include "kv8.cuh"
 
 #include <climits>
