@@ -129,6 +129,13 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Natural logarithm of l 2^ref, where l is near 2^bias and ref near -bias: the
+// whole bias (exact in both) goes before the logarithm, so that a sum near one
+// keeps its last digits.
+__device__ __forceinline__ float log_sum(float ref, float l, float bias) {
+  return ((ref + bias) + log2f(l * exp2_whole(-bias))) * kLn2;
+}
+
 // Key splits of a row: split s gives o_s = sum 2^(x - ref_s) v8 and (ref_s,
 // l_s) with l_s = sum 2^(x - ref_s) / vs; where a split shows the row nothing,
 // l_s = 0 and o_s is zero or was not written (each kernel says which).

@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(NT)) rows_attention_k
       *reinterpret_cast<uint2*>(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col) =
           make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
       if (col == 0 && p.lse)
-        p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = lsum == 0.f ? -INFINITY : (ref + log2f(lsum)) * kLn2;
+        p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = lsum == 0.f ? -INFINITY : log_sum(ref, lsum, kPBias);
     }
   }
 }
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const __grid_co
   *reinterpret_cast<uint2*>(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col * 4) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   if (col == 0 && p.lse)
-    p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = lsum == 0.f ? -INFINITY : (ref + log2f(lsum)) * kLn2;
+    p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = lsum == 0.f ? -INFINITY : log_sum(ref, lsum, kPBias);
 }
 
 // ------------------------------------------------------------------ weighing

@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (splits > 1)
           p.part_ml[pr] = make_float2(none ? -INFINITY : ref, l);
         else if (p.lse)
-          p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = none ? -INFINITY : (ref + log2f(l)) * kLn2;
+          p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = none ? -INFINITY : log_sum(ref, l, kTileBias);
       }
       __nv_bfloat16* dst = p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD;
       float* pdst = p.part_o + pr * HD;
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(kTileJoinThreads) tile_join_kernel(const __gri
   *reinterpret_cast<uint2*>(p.o + (b * p.o_bstride + qi) * p.ld_o + (int64_t)h * HD + col) =
       make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
   if (col == 0 && p.lse)
-    p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+    p.lse[((int64_t)b * p.n_heads + h) * p.n_q + qi] = l == 0.f ? -INFINITY : log_sum(ref, l, kTileBias);
 }
 
 // ------------------------------------------------------------------ weighing

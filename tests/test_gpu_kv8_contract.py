@@ -272,3 +272,18 @@ def test_replacing_a_tensor_is_refused_and_copying_the_new_lengths_works():
     q = queries(271, 1, 40, 4, 64) * 0.2
     assert torch.equal(a.lens, b.lens) and torch.equal(wa, wb)
     assert torch.equal(a.attend(q)[0], b.attend(q)[0])
+
+
+# ------------------------------------------------------------------ short caches
+
+@pytest.mark.parametrize("n", [1, 7, 30, 300])
+@pytest.mark.parametrize("group", [1, 8])
+def test_lse_of_a_few_keys_keeps_its_digits(n, group):
+    """Sums near one, logarithms near zero: what the weights are kept times must not cost lse its last digits."""
+    for seed in range(6):
+        lens = [1, 2, 3, 1, 5, 2]
+        c = scattered(6, 5, 8, 64, 64, lens, seed=280 + seed)
+        for scale in (0.2, 0.02):
+            q = (queries(290 + seed, 6, n, 8 * group, 64) * scale).to(torch.bfloat16)
+            check_attend(c, q, lens, False)
+            check_attend(c, q, lens, True)
