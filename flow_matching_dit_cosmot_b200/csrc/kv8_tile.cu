@@ -20,12 +20,12 @@
 // m the running maximum of x; it is followed only when it grows by more than
 // 2^5, so p 2^y stays below 2^15.  l = sum (p 2^y) / 2^y stays in float32.
 // Where the value scales of a CTA's keys lie within 2^2 of one another (warp 0
-// looks at them all while the queries come in), y = log2 vs: f16 keeps full
-// precision down to 2^-22 of the largest weight, a step of 2^-32 of it below.
-// Otherwise vs = 2^(y + shift + unit) with -1 < y <= 0: V's tile is widened times
-// 2^shift, exact from 2^-15 to 2^7, and O is in units of 2^unit, which moves from
-// tile to tile so that the tile's scales fit (O changes by a power of two then,
-// like for a maximum that moved).  Only blocks of one tile further apart than
+// looks at them all while the queries come in), vs = 2^(y + unit), unit the
+// largest's log2 and O in units of 2^unit: f16 keeps full precision down to 2^-22
+// of the largest weight, a step of 2^-32 of it below.  Otherwise vs = 2^(y + shift
+// + unit) with -1 < y <= 0: V's tile is widened times 2^shift, exact from 2^-15 to
+// 2^7, and the unit moves from tile to tile so that the tile's scales fit (O
+// changes by a power of two then, like for a maximum that moved).  Only blocks of one tile further apart than
 // 2^22 leave a rest in y, and the smaller ones' weights lose digits by it.
 // 1,560 queries x 14,106 rows x 32 heads: 365 us with near scales, 380 with random
 // ones in 2^4, 427 in 2^40; 363 where any spread went into y, which is wrong for
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const uint32_t bar_o_done = bar_p_full + 16;            // [1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 1 + 2 * kSlots + 7);
   const uint32_t bar_span = smem_u32(bars + 24);            // [1] vs_top is written
-  int32_t* vs_top = reinterpret_cast<int32_t*>(bars + 25);  // log2 of the largest value scale; INT_MIN: all are near
+  volatile int32_t* vs_top = reinterpret_cast<int32_t*>(bars + 25);  // log2 of the largest value scale; whether all are near
   // [4][NG] (ks, y, 2^-y, unit)
   float4* scales = reinterpret_cast<float4*>(smem + (2 + kSlots) * C::kTileBytes + 256);
   constexpr int kGroupKeys = kTile / NG;
@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         scale_log2_parts(__int_as_float(hi), top, inv);
         scale_log2_parts(__int_as_float(lo), low, inv);
         if (lane == 0) {
-          *vs_top = top - low > kFold ? (int)ceilf(top) : INT_MIN;
+          vs_top[0] = (int)ceilf(top);
+          vs_top[1] = top - low <= kFold;
           mbar_arrive(bar_span);
         }
         __syncwarp();
@@ -361,10 +362,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       load(wk, kp, left_k);
       load(wv, vp, left_v);
     }
-    int32_t top = INT_MIN;
-    if (n_vis > 0 && warp_wait(bar_span, 0, p.status, kWhereKv8Widen)) top = *reinterpret_cast<volatile int32_t*>(vs_top);
-    if (top != INT_MIN) {
-      int unit = top;  // (every warp finds the same units and shifts: nothing is exchanged for them)
+    if (n_vis > 0 && warp_wait(bar_span, 0, p.status, kWhereKv8Widen) && !vs_top[1]) {
+      int unit = vs_top[0];  // (every warp finds the same units and shifts: nothing is exchanged for them)
 #pragma unroll 1
       for (int j = 0; j < n_vis; ++j) {
         float4 sc = make_float4(1.f, 0.f, 0.f, 0.f);  // a group behind the end: finite, and every key masked
@@ -398,11 +397,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     } else {
       for (int j = 0; j < n_vis; ++j) {
         const int32_t kt = kt0 + j;
-        float4 sc = make_float4(1.f, 0.f, 0.f, 0.f);  // a group behind the end: finite, and every key masked
+        float4 sc = make_float4(1.f, 0.f, 0.f, (float)vs_top[0]);  // a group behind the end: finite, and every key masked
         if (cw == 0 && lane < NG && kt * kTile + lane * kGroupKeys < kend) {
           const int64_t at = (int64_t)bg * c.n_blocks + kt * NG + lane;
           sc.x = load_global(c.k_scale + at);
           scale_log2_parts(load_global(c.v_scale + at), sc.y, sc.z);
+          sc.y -= sc.w;
+          sc.z *= exp2_whole(sc.w);
         }
         if (!empty(2 * j)) break;
         widen(wk, (2 * j) % kSlots);
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           m_new = fmaxf(m_new, fmaf(x, fac * k.x, k.y));
         }
         const float unit_now = sc[0].w;
-        const bool moved = unit_now != unit;  // (before the first product too, which does not read O)
+        const bool moved = unit_now != unit && j > 0;
         const bool first = m == -INFINITY;
         const bool need = !first && m_new > m + kFollow;
         float factor = 1.f;
@@ -545,7 +546,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         if (__any_sync(0xffffffffu, need || moved)) {
           if (moved) factor *= exp2_whole(fminf(fmaxf(unit - unit_now, -126.f), 126.f));
-          unit = unit_now;
 #pragma unroll 1
           for (int i = 0; i < HD / 32; ++i) {
             uint32_t ov[32];
@@ -557,6 +557,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           tmem_st_wait();
         }
+        unit = unit_now;
         const float mu = m == -INFINITY ? 0.f : m - kTileBias;
 #pragma unroll
         for (int g2 = 0; g2 < 4; ++g2) {  // 32 keys

@@ -287,3 +287,16 @@ def test_lse_of_a_few_keys_keeps_its_digits(n, group):
             q = (queries(290 + seed, 6, n, 8 * group, 64) * scale).to(torch.bfloat16)
             check_attend(c, q, lens, False)
             check_attend(c, q, lens, True)
+
+
+@pytest.mark.parametrize("n", [1, 40, 300])
+@pytest.mark.parametrize("exponent", [-31, 25])
+def test_lse_does_not_depend_on_the_size_of_the_values(n, exponent):
+    lens = [1, 2, 17, 91]
+    for seed in range(4):
+        c = scattered(4, 100, 8, 64, 16, lens, seed=300 + seed)
+        q = (queries(310 + seed, 4, n, 16, 64) * 0.2).to(torch.bfloat16)
+        _, lse = check_attend(c, q, lens, False)
+        c.v_scale.mul_(2.0 ** exponent)
+        _, far = check_attend(c, q, lens, False)
+        assert torch.equal(lse, far)
