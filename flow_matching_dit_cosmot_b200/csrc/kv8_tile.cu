@@ -25,8 +25,9 @@
 // of the largest weight, a step of 2^-32 of it below.  Otherwise vs = 2^(y + shift
 // + unit) with -1 < y <= 0: V's tile is widened times 2^shift, exact from 2^-15 to
 // 2^7, and the unit moves from tile to tile so that the tile's scales fit (O
-// changes by a power of two then, like for a maximum that moved).  Only blocks of one tile further apart than
-// 2^22 leave a rest in y, and the smaller ones' weights lose digits by it.
+// changes by a power of two then, like for a maximum that moved).  Only blocks of
+// one tile further apart than 2^22 leave a rest in y, and the smaller ones'
+// weights lose digits by it.
 // 1,560 queries x 14,106 rows x 32 heads: 365 us with near scales, 380 with random
 // ones in 2^4, 427 in 2^40; 363 where any spread went into y, which is wrong for
 // far ones.  P as two bf16 where scales are far took 10 % more with near ones too
@@ -36,7 +37,7 @@
 // alone 2,048).  The same sizes: 409 us = 880 TFLOP/s in long runs under the power
 // cap, 365 us (986) on a cool card; tensor pipe and SFU at 50 %.
 // Registers a thread: 176 for the softmax and 80 for the other warps measured
-// best (184 / 72 +2 %, 192 / 64 +6 %, 168 / 88 the same).
+// best (184 / 72 +2 %, 192 / 64 +6 %, 168 / 88 +5 %).
 //
 // Weighing.  One CTA per (sequence, key head, 256 keys): the keys are widened
 // to bf16 once and stay in smem, the queries' tiles come by TMA as they are
