@@ -24,12 +24,12 @@
 // precision for weights down to 2^-22 of the largest, and a step of 2^-32 of it
 // below.  O^T is in those units too.  A block whose scale lies outside the window
 // moves it: the accumulators change by a power of two, which float32 holds
-// exactly, so that scales far apart cost the weights no digits.  (The window costs
-// 0.5 % for one token and 4 % at 32 rows x 32 heads; with every scale in the
-// exponent, whatever their spread, small ones lose their digits.  A window of one power took 10 % more where
-// neighbouring blocks differ by one; to bring every 16 keys' share in by its own
-// scale 2 % and 12 %; to follow the maximum at 2^7 saves 1.5 % and costs three
-// digits.)
+// exactly, so that scales far apart cost the weights no digits.  (It costs 0.5 %
+// for one token and 4 % at 32 rows x 32 heads; with every scale in the exponent,
+// whatever their spread, small ones lose their digits.  A unit that follows every
+// block's scale took 10 % more where neighbours differ by one; to bring every 16
+// keys' share in by its own scale 2 % and 12 %; to follow the maximum at 2^7 saves
+// 1.5 % and costs three digits.)
 #include "kv8.cuh"
 
 #include <mutex>
